@@ -2,7 +2,7 @@
 
 Argument marshalling only: every step of the layer runs in the library's HIP
 kernels.  PyTorch provides device memory and the current stream.  The
-functions mirror the C ABI in include/moe.h one to one; ``Buffers``,
+functions mirror the C ABI in include/moe.h and include/moe_i8.h one to one; ``Buffers``,
 ``forward`` and ``backward`` allocate the tensors of one layer pass and chain
 the entry points in order.
 
@@ -17,7 +17,7 @@ import os
 import torch  # imported before libmoe.so so that the process holds one HIP runtime
 
 __all__ = [
-    "MoeError", "MoeDesc", "lib", "make_desc", "new_tile_counters", "SCHEDULE_STATIC", "SCHEDULE_DYNAMIC", "workspace_size", "router_logits", "route", "route_grouped", "hold_cus", "fp8_quantize", "fp8_dequantize", "permute", "permute_noalloc", "expert_gate_up_gather", "grouped_ffn_bwd_dw_gather", "expert_gate_up_fp8", "expert_down_fp8", "fp8_quantize_pow2", "expert_gate_up_fp8mm", "fp8_quantize_pow2_rows", "expert_down_fp8mm", "fp8_scale_row_bytes", "row_weights", "dtopk_w_from_parts", "dtopk_parts",
+    "MoeError", "MoeDesc", "lib", "make_desc", "new_tile_counters", "SCHEDULE_STATIC", "SCHEDULE_DYNAMIC", "workspace_size", "router_logits", "route", "route_grouped", "hold_cus", "fp8_quantize", "fp8_dequantize", "permute", "permute_noalloc", "expert_gate_up_gather", "grouped_ffn_bwd_dw_gather", "expert_gate_up_fp8", "expert_down_fp8", "fp8_quantize_pow2", "expert_gate_up_fp8mm", "fp8_quantize_pow2_rows", "expert_down_fp8mm", "fp8_scale_row_bytes", "i8_quantize_rows", "i8_linear", "expert_gate_up_i8", "expert_down_i8", "Int8Experts", "Int8Buffers", "forward_i8", "row_weights", "dtopk_w_from_parts", "dtopk_parts",
     "grouped_ffn", "expert_gate_up", "expert_down", "expert_bwd_dh", "expert_bwd_dx", "expert_bwd_dw_gate_up", "expert_bwd_dw_down", "combine_bwd_gather", "expert_bwd_dh_gather", "expert_bwd_dw_down_gather", "combine", "combine_bwd", "grouped_ffn_bwd_dx", "grouped_ffn_bwd_dw",
     "unpermute_bwd", "unpermute_router_bwd", "route_bwd", "router_bwd", "router_bwd_acc", "Buffers", "forward", "backward",
     "MOE_F32", "MOE_BF16",
@@ -108,6 +108,12 @@ _SIGS = {
 EXPORTS = sorted(list(_SIGS) + ["moe_workspace_size", "moe_status_str", "moe_last_error", "moe_hold_cus",
                                  "moe_fp8_quantize", "moe_fp8_dequantize", "moe_fp8_quantize_pow2",
                                  "moe_fp8_quantize_pow2_rows"])
+# include/moe_i8.h
+_SIGS_I8 = {
+    "moe_expert_gate_up_i8": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "moe_expert_down_i8": [_vp, _vp, _vp, _vp, _vp, _vp, _vp],
+}
+EXPORTS_I8 = sorted(list(_SIGS_I8) + ["moe_i8_quantize_rows", "moe_i8_linear"])
 
 _lib = None
 
@@ -119,7 +125,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing; build it with __graft_entry__.build()")
         l = ctypes.CDLL(LIB_PATH)
-        for name, args in _SIGS.items():
+        for name, args in {**_SIGS, **_SIGS_I8}.items():
             fn = getattr(l, name)
             fn.argtypes = [ctypes.POINTER(MoeDesc)] + args
             fn.restype = ctypes.c_int
@@ -136,6 +142,12 @@ def lib():
                                                  ctypes.c_int64, _vp]
         l.moe_fp8_quantize_pow2_rows.restype = ctypes.c_int
         l.moe_fp8_dequantize.restype = ctypes.c_int
+        l.moe_i8_quantize_rows.argtypes = [_vp, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, _vp,
+                                           ctypes.c_int64, _vp, _vp]
+        l.moe_i8_quantize_rows.restype = ctypes.c_int
+        l.moe_i8_linear.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, ctypes.c_int64, _vp, _vp,
+                                    ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int, _vp]
+        l.moe_i8_linear.restype = ctypes.c_int
         l.moe_hold_cus.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp]
         l.moe_hold_cus.restype = ctypes.c_int
         l.moe_last_error.argtypes = []
@@ -264,6 +276,86 @@ def expert_down_fp8mm(desc, offsets, hq, hs, w2q, w2s, y_perm):
 def expert_gate_up_fp8mm(desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, gu, h):
     """gate/up + SwiGLU on the FP8 matrix cores: x and W1/W3 as codes with E8M0 block scales."""
     _call("moe_expert_gate_up_fp8mm", desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, gu, h, _stream())
+
+
+def _here(t, name):
+    """The INT8 calls launch on the current device: a tensor of another one is refused."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor of the current device is needed, not of {t.device}")
+
+
+def _rows(t, name, dtypes):
+    """The distance in elements of the rows of a 2-D tensor (a row's values lie together)."""
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name}: a 2-D tensor of {' or '.join(str(d) for d in dtypes)} is needed")
+    _here(t, name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must lie together")
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _flat(t, name, n, dtype):
+    """The address of a contiguous tensor of at least n values."""
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor of at least {n} {dtype} is needed")
+    _here(t, name)
+    return t.data_ptr()
+
+
+def i8_quantize_rows(w, q, scale, nrows=None):
+    """INT8 codes q and scales of the rows of w [rows][cols] (bf16 or fp32):
+    code = 127 w / max|row| (ties to even), scale = max|row| / 127.  Rows of w
+    and q may lie apart (q's by a multiple of 16); rows at or past the device
+    int32 nrows (if given) are left alone."""
+    ldw = _rows(w, "w", (torch.bfloat16, torch.float32))
+    ldq = _rows(q, "q", (torch.int8,))
+    rows, cols = w.shape
+    if q.shape != w.shape:
+        raise ValueError("q must have w's shape")
+    if rows == 0:
+        return
+    rc = lib().moe_i8_quantize_rows(w.data_ptr(), MOE_BF16 if w.dtype == torch.bfloat16 else MOE_F32, rows, cols, ldw,
+                                    None if nrows is None else _flat(nrows, "nrows", 1, torch.int32), q.data_ptr(),
+                                    ldq, _flat(scale, "scale", rows, torch.float32), _stream())
+    if rc != MOE_OK:
+        raise MoeError("moe_i8_quantize_rows", rc)
+
+
+def i8_linear(xq, xs, wq, ws, y, bias=None):
+    """y [M][N] (bf16 or fp32) = xs ws (xq wq^T) + bias from codes xq [M][K],
+    wq [N][K] (rows apart by multiples of 16) and float32 scales xs [M], ws [N]."""
+    ldx, ldw = _rows(xq, "xq", (torch.int8,)), _rows(wq, "wq", (torch.int8,))
+    ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
+    (M, K), N = xq.shape, wq.shape[0]
+    if wq.shape[1] != K or y.shape != (M, N):
+        raise ValueError("xq [M][K], wq [N][K] and y [M][N] do not fit")
+    if M == 0:
+        return
+    rc = lib().moe_i8_linear(M, N, K, xq.data_ptr(), ldx, _flat(xs, "xs", M, torch.float32), wq.data_ptr(), ldw,
+                             _flat(ws, "ws", N, torch.float32), None if bias is None else _flat(bias, "bias", N, torch.float32), y.data_ptr(),
+                             ldy, MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, _stream())
+    if rc != MOE_OK:
+        raise MoeError("moe_i8_linear", rc)
+
+
+def expert_gate_up_i8(desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, gu, h):
+    """gate/up + SwiGLU on INT8 codes with a scale per token and per channel."""
+    T, d, f, NL, Rc = desc.T, desc.d, desc.f, desc.num_local, desc.R_cap
+    i8, f32, bf = torch.int8, torch.float32, torch.bfloat16
+    _call("moe_expert_gate_up_i8", desc, _flat(offsets, "offsets", NL + 1, torch.int32),
+          _flat(row_token, "row_token", Rc, torch.int32), _flat(xq, "xq", T * d, i8), _flat(xs, "xs", T, f32),
+          _flat(w1q, "w1q", NL * f * d, i8), _flat(w1s, "w1s", NL * f, f32), _flat(w3q, "w3q", NL * f * d, i8),
+          _flat(w3s, "w3s", NL * f, f32), None if gu is None else _flat(gu, "gu", Rc * 2 * f, bf),
+          _flat(h, "h", Rc * f, bf), _stream())
+
+
+def expert_down_i8(desc, offsets, hq, hs, w2q, w2s, y_perm):
+    """down on INT8 codes with a scale per row and per channel."""
+    d, f, NL, Rc = desc.d, desc.f, desc.num_local, desc.R_cap
+    _call("moe_expert_down_i8", desc, _flat(offsets, "offsets", NL + 1, torch.int32),
+          _flat(hq, "hq", Rc * f, torch.int8), _flat(hs, "hs", Rc, torch.float32),
+          _flat(w2q, "w2q", NL * d * f, torch.int8), _flat(w2s, "w2s", NL * d, torch.float32),
+          _flat(y_perm, "y_perm", Rc * d, torch.bfloat16), _stream())
 
 
 def fp8_dequantize(q, scales, w):
@@ -487,6 +579,53 @@ def forward(b: Buffers, x, wr, w1, w3, w2, bias=None, routing=None, n_groups=1):
     else:
         permute(D, idx, x, b.counts, b.offsets, b.row_token, b.slot_row, b.x_perm, b.ws_permute)
         grouped_ffn(D, b.offsets, b.x_perm, w1, w3, w2, b.gu, b.h, b.y_perm)
+    combine(D, b.slot_row, w, b.y_perm, b.y)
+    return b.y
+
+
+class Int8Experts:
+    """The experts' weights as INT8 codes with one scale per channel, made once
+    from W1, W3 [NL][f][d] and W2 [NL][d][f]."""
+
+    def __init__(self, w1, w3, w2):
+        for name, w in (("w1", w1), ("w3", w3), ("w2", w2)):
+            n, rows, cols = w.shape
+            q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+            s = torch.empty(n, rows, dtype=torch.float32, device=w.device)
+            i8_quantize_rows(w.view(n * rows, cols), q.view(n * rows, cols), s.view(-1))
+            setattr(self, name + "q", q)
+            setattr(self, name + "s", s)
+
+
+class Int8Buffers:
+    """Codes and scales of one INT8 forward pass, beside its Buffers."""
+
+    def __init__(self, desc: MoeDesc, device="cuda"):
+        self.xq = torch.empty(desc.T, desc.d, dtype=torch.int8, device=device)
+        self.xs = torch.empty(desc.T, dtype=torch.float32, device=device)
+        self.hq = torch.empty(desc.R_cap, desc.f, dtype=torch.int8, device=device)
+        self.hs = torch.empty(desc.R_cap, dtype=torch.float32, device=device)
+
+
+def forward_i8(b: Buffers, i8: Int8Buffers, x, wr, experts: Int8Experts, bias=None, routing=None, n_groups=1):
+    """forward with the expert products in INT8: the router, the permutation's
+    indices and the combine as there, x and h quantised per row on the way."""
+    D = b.desc
+    if routing is None:
+        router_logits(D, x, wr, bias, b.logits, b.ws_router)
+        if n_groups > 1:
+            route_grouped(D, b.logits, n_groups, b.topk_idx, b.topk_w)
+        else:
+            route(D, b.logits, b.topk_idx, b.topk_w)
+        idx, w = b.topk_idx, b.topk_w
+    else:
+        idx, w = routing
+    permute(D, idx, None, b.counts, b.offsets, b.row_token, b.slot_row, None, b.ws_permute)
+    i8_quantize_rows(x, i8.xq, i8.xs)
+    expert_gate_up_i8(D, b.offsets, b.row_token, i8.xq, i8.xs, experts.w1q, experts.w1s, experts.w3q, experts.w3s,
+                      b.gu, b.h)
+    i8_quantize_rows(b.h, i8.hq, i8.hs, nrows=b.offsets[-1:])
+    expert_down_i8(D, b.offsets, i8.hq, i8.hs, experts.w2q, experts.w2s, b.y_perm)
     combine(D, b.slot_row, w, b.y_perm, b.y)
     return b.y
 

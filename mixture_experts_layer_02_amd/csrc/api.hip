@@ -439,6 +439,54 @@ int moe_expert_down_fp8mm(const moe_desc* desc, const int32_t* offsets, const ui
   return finish(moe::launch_down_f8(*desc, offsets, hq, hs, W2q, W2s, y_perm, S(stream)));
 }
 
+// Sums of K products of codes up to 127 fit 32-bit integers; rows of codes are
+// addressed with 32-bit offsets within a tile.
+constexpr int64_t I8_MAX_K = 1 << 17, I8_MAX_LD = 1 << 22;
+
+int moe_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw, const int32_t* nrows,
+                         int8_t* q, int64_t ldq, float* scale, void* stream) {
+  if (!need(w) || !need(q) || !scale || (reinterpret_cast<uintptr_t>(scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(nrows) & 3u) || rows < 0 || cols < 1 || ldw < cols || ldq < cols || ldq % 16)
+    return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  return finish(moe::launch_i8_quantize_rows(w, dtype, rows, cols, ldw, nrows, q, ldq, scale, S(stream)));
+}
+
+int moe_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq,
+                  int64_t ldw, const float* ws, const float* bias, void* y, int64_t ldy, int dtype, void* stream) {
+  if (!need(xq) || !need(xs) || !need(wq) || !need(ws) || !opt(bias) || !need(y) || M < 0 || N < 1 || K < 1 ||
+      ldx < K || ldw < K || ldy < N || ldx % 16 || ldw % 16)
+    return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (K > I8_MAX_K || ldx > I8_MAX_LD || ldw > I8_MAX_LD || M >= (1ll << 31) - 256 || N >= (1ll << 31) - 256)
+    return MOE_ERR_UNSUPPORTED;
+  return finish(moe::launch_i8_linear(M, N, K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, S(stream)));
+}
+
+int moe_expert_gate_up_i8(const moe_desc* desc, const int32_t* offsets, const int32_t* row_token, const int8_t* xq,
+                          const float* xs, const int8_t* W1q, const float* W1s, const int8_t* W3q, const float* W3s,
+                          void* gu, void* h, void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  if (!need(offsets) || !need(row_token) || !need(xq) || !need(xs) || !need(W1q) || !need(W1s) || !need(W3q) ||
+      !need(W3s) || !opt(gu) || !need(h))
+    return MOE_ERR_INVALID_ARG;
+  // bf16 outputs; the gathered codes addressed in 32 bits
+  if (desc->dtype != MOE_BF16 || desc->d > I8_MAX_K || (int64_t)desc->T * desc->d >= (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return finish(moe::launch_gate_up_i8(*desc, offsets, row_token, xq, xs, W1q, W1s, W3q, W3s, gu, h, S(stream)));
+}
+
+int moe_expert_down_i8(const moe_desc* desc, const int32_t* offsets, const int8_t* hq, const float* hs,
+                       const int8_t* W2q, const float* W2s, void* y_perm, void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  if (!need(offsets) || !need(hq) || !need(hs) || !need(W2q) || !need(W2s) || !need(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  if (desc->dtype != MOE_BF16 || desc->f > I8_MAX_K) return MOE_ERR_UNSUPPORTED;
+  return finish(moe::launch_down_i8(*desc, offsets, hq, hs, W2q, W2s, y_perm, S(stream)));
+}
+
 int moe_hold_cus(int workgroups, int lds_bytes, int microseconds, void* stream) {
   if (workgroups < 1 || workgroups > 4096 || lds_bytes < 4 || lds_bytes > 160 * 1024 || microseconds < 0 ||
       microseconds > 1000000)

@@ -25,6 +25,16 @@ hipError_t launch_down_q8(const moe_desc& d, const int32_t* offsets, const void*
 hipError_t launch_fp8_quantize(const void* w, int dtype, int64_t n, uint8_t* q, float* scales, hipStream_t s);
 hipError_t launch_fp8_dequantize(const uint8_t* q, const float* scales, int64_t n, void* w, hipStream_t s);
 hipError_t launch_fp8_quantize_pow2(const void* w, int dtype, int64_t n, uint8_t* q, uint8_t* e8, hipStream_t s);
+hipError_t launch_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw,
+                                   const int32_t* nrows, int8_t* q, int64_t ldq, float* scale, hipStream_t s);
+hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const int32_t* row_token, const int8_t* xq,
+                             const float* xs, const int8_t* W1q, const float* W1s, const int8_t* W3q,
+                             const float* W3s, void* gu, void* h, hipStream_t s);
+hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_t* hq, const float* hs,
+                          const int8_t* W2q, const float* W2s, void* y_perm, hipStream_t s);
+hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, int64_t ldx, const float* xs,
+                            const int8_t* wq, int64_t ldw, const float* ws, const float* bias, void* y, int64_t ldy,
+                            int dtype, hipStream_t s);
 
 size_t permute_workspace(const moe_desc& d);
 // Size of the allocation-free permute's fixed device scratch (4 MiB per device).

@@ -49,6 +49,7 @@ __all__ = [
     "silu", "silu_grad", "expert_ffn_rows", "expert_ffn", "expert_down", "combine",
     "combine_bwd", "expert_ffn_bwd_rows", "expert_ffn_bwd", "unpermute_bwd",
     "route_bwd", "router_bwd", "layer_forward", "layer_backward",
+    "i8_quantize_rows", "i8_dequantize_rows", "i8_linear",
 ]
 
 
@@ -601,3 +602,36 @@ def layer_backward(fwd, x, wr, w1, w3, w2, dy, renormalize=1):
     dx_r, dWr = router_bwd(x, wr, dL)
     return dict(dy_perm=dy_perm, dw=dw, dG=dG, dU=dU, dx_perm=dXp, dW1=dW1, dW3=dW3,
                 dW2=dW2, dlogits=dL, dx_router=dx_r, dx=dx_moe + dx_r, dWr=dWr)
+
+
+# --------------------------------------------------------------------------
+# INT8 codes with one scale per row (per token, per output channel).
+# --------------------------------------------------------------------------
+def i8_quantize_rows(w):
+    """codes [rows][cols] int8 and scales [rows] float32 of w [rows][cols].
+
+    Per row with m = max |w|: scale = m / 127 (float32), code = 127 w / m to
+    the nearest integer, ties to even.  The quotient is taken in float64: for
+    float32 values its distance from a tie is 0 or above 2^-40 of it, so
+    float64 decides as the exact quotient does.  A row of zeros has scale 0; a
+    row that is not finite has scale NaN; both have codes 0.
+    """
+    w = np.asarray(w, np.float32)
+    m = np.abs(w).max(axis=1).astype(np.float64)
+    live = np.isfinite(m) & (m > 0)
+    with np.errstate(invalid="ignore"):
+        q = np.rint(w.astype(np.float64) * 127.0 / np.where(live, m, 1.0)[:, None])
+    codes = np.where(live[:, None], q, 0.0).astype(np.int8)
+    scale = np.where(np.isfinite(m), m.astype(np.float32) / np.float32(127), np.float32(np.nan)).astype(np.float32)
+    return codes, scale
+
+
+def i8_dequantize_rows(codes, scale):
+    """The float64 values the codes stand for."""
+    return np.asarray(codes, np.float64) * np.asarray(scale, np.float64)[..., None]
+
+
+def i8_linear(xq, xs, wq, ws, bias=None):
+    """y [M][N] = xs ws (xq wq^T) + bias: the product of whole numbers is exact in float64."""
+    y = (_f64(xq) @ _f64(wq).T) * _f64(xs)[:, None] * _f64(ws)[None, :]
+    return y if bias is None else y + _f64(bias)[None, :]

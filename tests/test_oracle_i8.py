@@ -1,0 +1,147 @@
+"""Pins of the INT8 oracle, and the INT8 entry points' refusals (no GPU)."""
+import ctypes
+import os
+import re
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_02_amd as moe
+import oracle
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _exact_code(v, m):
+    """127 v / m to the nearest integer, ties to even, in rational arithmetic."""
+    return round(Fraction(float(v)) * 127 / Fraction(float(m)))
+
+
+def test_codes_are_the_exact_quotients():
+    rng = np.random.default_rng(0)
+    rows = [rng.normal(0, 1, 64).astype(np.float32) for _ in range(40)]
+    for m in (np.float32(254.0), np.float32(127 * 2.0 ** -20), np.float32(1.7), np.float32(3e-39), np.float32(3e38)):
+        n = rng.integers(-126, 126, 20)
+        near = (n + 0.5) / 127.0 * np.float64(m)
+        v = near.astype(np.float32)                            # at, just below and just above a tie
+        rows.append(np.concatenate([v, np.nextafter(v, np.float32(-3e38)), np.nextafter(v, np.float32(3e38)),
+                                    [m, -m, 0, 0]]).astype(np.float32))
+    w = np.stack(rows)
+    codes, scale = oracle.i8_quantize_rows(w)
+    for r in range(len(rows)):
+        m = np.abs(w[r]).max()
+        assert scale[r] == np.float32(m) / np.float32(127)
+        for c in range(64):
+            assert codes[r, c] == _exact_code(w[r, c], m), (r, c)
+
+
+def test_the_largest_value_is_127_and_the_error_half_a_step():
+    rng = np.random.default_rng(1)
+    w = rng.normal(0, 3, (50, 200)).astype(np.float32)
+    codes, scale = oracle.i8_quantize_rows(w)
+    assert (np.abs(codes.astype(int)).max(axis=1) == 127).all()
+    err = np.abs(oracle.i8_dequantize_rows(codes, scale) - w.astype(np.float64))
+    # half a step, and the scale's own rounding (2^-24 of up to 127 steps)
+    assert (err <= scale[:, None].astype(np.float64) * (0.5 + 127 * 2.0 ** -23)).all()
+
+
+def test_zero_and_not_finite_rows():
+    w = np.array([[0, -0.0, 0], [1, np.inf, 2], [np.nan, 1, 2], [-np.inf, np.nan, 0], [0, 0, -2]], np.float32)
+    codes, scale = oracle.i8_quantize_rows(w)
+    assert (codes[:4] == 0).all() and codes[4].tolist() == [0, 0, -127]
+    assert scale[0] == 0 and np.isnan(scale[1:4]).all() and scale[4] == np.float32(2) / np.float32(127)
+
+
+def test_linear_by_hand():
+    y = oracle.i8_linear([[1, -2], [3, 4]], [0.5, 2.0], [[5, 6], [-7, 8], [0, 1]], [1.0, 0.25, 3.0], [1.0, 0.0, -1.0])
+    np.testing.assert_array_equal(y, [[0.5 * -7 + 1, 0.125 * -23, 1.5 * -2 - 1], [2 * 39 + 1, 0.5 * 11, 6 * 4 - 1]])
+
+
+# ---- the entry points without a GPU ---------------------------------------
+
+def test_header_and_exports_agree():
+    with open(os.path.join(ROOT, "include", "moe_i8.h")) as fh:
+        names = sorted(set(re.findall(r"^int (moe_\w+)\s*\(", fh.read(), re.M)))
+    assert names == moe.EXPORTS_I8
+    for n in names:
+        assert hasattr(moe.lib(), n), n
+
+
+P = 4096  # a 16-byte aligned address that no rejected call reads
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(w=None), moe.MOE_ERR_INVALID_ARG), (dict(q=None), moe.MOE_ERR_INVALID_ARG),
+    (dict(scale=None), moe.MOE_ERR_INVALID_ARG), (dict(w=P + 2), moe.MOE_ERR_INVALID_ARG),
+    (dict(q=P + 8), moe.MOE_ERR_INVALID_ARG), (dict(scale=P + 2), moe.MOE_ERR_INVALID_ARG),
+    (dict(nrows=P + 1), moe.MOE_ERR_INVALID_ARG), (dict(rows=-1), moe.MOE_ERR_INVALID_ARG),
+    (dict(cols=0), moe.MOE_ERR_INVALID_ARG), (dict(ldw=99), moe.MOE_ERR_INVALID_ARG),
+    (dict(ldq=96), moe.MOE_ERR_INVALID_ARG), (dict(ldq=120), moe.MOE_ERR_INVALID_ARG),
+    (dict(dtype=2), moe.MOE_ERR_UNSUPPORTED), (dict(dtype=-1), moe.MOE_ERR_UNSUPPORTED),
+    (dict(rows=0), moe.MOE_OK),
+])
+def test_quantize_refusals(kw, rc):
+    a = dict(w=P, dtype=moe.MOE_BF16, rows=4, cols=100, ldw=100, nrows=None, q=P, ldq=112, scale=P)
+    a.update(kw)
+    assert moe.lib().moe_i8_quantize_rows(a["w"], a["dtype"], a["rows"], a["cols"], a["ldw"], a["nrows"], a["q"],
+                                          a["ldq"], a["scale"], None) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [(dict([(n, None)]), moe.MOE_ERR_INVALID_ARG) for n in ("xq", "xs", "wq", "ws", "y")] + [
+    (dict([(n, P + 4)]), moe.MOE_ERR_INVALID_ARG) for n in ("xq", "xs", "wq", "ws", "bias", "y")] + [
+    (dict(M=-1), moe.MOE_ERR_INVALID_ARG), (dict(N=0), moe.MOE_ERR_INVALID_ARG), (dict(K=0), moe.MOE_ERR_INVALID_ARG),
+    (dict(ldx=48), moe.MOE_ERR_INVALID_ARG), (dict(ldx=72), moe.MOE_ERR_INVALID_ARG),
+    (dict(ldw=48), moe.MOE_ERR_INVALID_ARG), (dict(ldw=72), moe.MOE_ERR_INVALID_ARG),
+    (dict(ldy=8), moe.MOE_ERR_INVALID_ARG), (dict(dtype=2), moe.MOE_ERR_UNSUPPORTED),
+    (dict(K=131073, ldx=131088, ldw=131088), moe.MOE_ERR_UNSUPPORTED),
+    (dict(ldx=4194320), moe.MOE_ERR_UNSUPPORTED), (dict(ldw=4194320), moe.MOE_ERR_UNSUPPORTED),
+    (dict(M=1 << 31), moe.MOE_ERR_UNSUPPORTED), (dict(N=1 << 31, ldy=1 << 31), moe.MOE_ERR_UNSUPPORTED),
+    (dict(M=0), moe.MOE_OK),
+])
+def test_linear_refusals(kw, rc):
+    a = dict(M=3, N=9, K=50, xq=P, ldx=64, xs=P, wq=P, ldw=64, ws=P, bias=None, y=P, ldy=9, dtype=moe.MOE_BF16)
+    a.update(kw)
+    assert moe.lib().moe_i8_linear(a["M"], a["N"], a["K"], a["xq"], a["ldx"], a["xs"], a["wq"], a["ldw"], a["ws"],
+                                   a["bias"], a["y"], a["ldy"], a["dtype"], None) == rc
+
+
+def test_expert_refusals():
+    l = moe.lib()
+    D = moe.make_desc(64, 128, 64, 8, 2, dtype="bf16")
+
+    def up(D, **kw):
+        a = dict.fromkeys(("offsets", "row_token", "xq", "xs", "w1q", "w1s", "w3q", "w3s", "gu", "h"), P)
+        a.update(kw)
+        return l.moe_expert_gate_up_i8(ctypes.byref(D), *a.values(), None)
+
+    def down(D, **kw):
+        a = dict.fromkeys(("offsets", "hq", "hs", "w2q", "w2s", "y"), P)
+        a.update(kw)
+        return l.moe_expert_down_i8(ctypes.byref(D), *a.values(), None)
+
+    for n in ("offsets", "row_token", "xq", "xs", "w1q", "w1s", "w3q", "w3s", "h"):
+        assert up(D, **{n: None}) == up(D, **{n: P + 8}) == moe.MOE_ERR_INVALID_ARG
+    assert up(D, gu=P + 8) == moe.MOE_ERR_INVALID_ARG
+    for n in ("offsets", "hq", "hs", "w2q", "w2s", "y"):
+        assert down(D, **{n: None}) == down(D, **{n: P + 8}) == moe.MOE_ERR_INVALID_ARG
+    for kw in (dict(dtype="f32"), dict(d=131072 + 64), dict(d=96)):
+        bad = moe.make_desc(**{**dict(T=64, d=128, f=64, E=8, k=2, dtype="bf16"), **kw})
+        assert up(bad) == moe.MOE_ERR_UNSUPPORTED
+    assert up(moe.make_desc(1 << 24, 128, 64, 8, 2, dtype="bf16")) == moe.MOE_ERR_UNSUPPORTED     # T d = 2^31
+    for kw in (dict(dtype="f32"), dict(f=131072 + 64)):
+        bad = moe.make_desc(**{**dict(T=64, d=128, f=64, E=8, k=2, dtype="bf16"), **kw})
+        assert down(bad) == moe.MOE_ERR_UNSUPPORTED
+    D.struct_size = 56
+    assert up(D) == down(D) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_python_refuses_host_tensors_and_wrong_types():
+    w, q, s = torch.zeros(4, 32), torch.zeros(4, 32, dtype=torch.int8), torch.zeros(4)
+    with pytest.raises(ValueError):
+        moe.i8_quantize_rows(w, q, s)                          # not on the GPU
+    with pytest.raises(ValueError):
+        moe.i8_quantize_rows(w.double(), q, s)
+    with pytest.raises(ValueError):
+        moe.i8_linear(q, s, q, s, torch.zeros(4, 4))
