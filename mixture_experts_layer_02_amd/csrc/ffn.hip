@@ -87,6 +87,21 @@ hipError_t run_bf16(const GemmParams& p, int64_t ub_tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
+// INT8 products (K counts pairs of codes): whole k-tiles, at least four.
+template <int GRP, int EPI, bool DUAL, bool CF32, int GATH>
+hipError_t run_i8_tiles(const GemmParams& p, int64_t ub_tiles, hipStream_t s) {
+  if (p.K % DMA_BK || p.K < 4 * DMA_BK) return hipErrorInvalidValue;
+  int64_t grid = std::min<int64_t>(ub_tiles, (int64_t)num_cus());
+  if (grid >= 8) grid -= grid % 8;
+  if (GRP == GRP_M && p.dyn)
+    gemm_dma_kernel<DMA_BK, DMA_STAGES, LAY_K, LAY_K, GRP, EPI, DUAL, CF32, GRP == GRP_M, GATH, false, false, true>
+        <<<(unsigned)grid, 256, 0, s>>>(p);
+  else
+    gemm_dma_kernel<DMA_BK, DMA_STAGES, LAY_K, LAY_K, GRP, EPI, DUAL, CF32, false, GATH, false, false, true>
+        <<<(unsigned)grid, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
 template <int ALAY, int BLAY, int GRP, int EPI, bool DUAL>
 hipError_t run_f32(const GemmParams& p, int64_t ub_tiles, hipStream_t s) {
   const int64_t grid = std::min<int64_t>(ub_tiles, (int64_t)num_cus() * 4);
@@ -351,6 +366,77 @@ hipError_t launch_down_f8(const moe_desc& d, const int32_t* offsets, const uint8
   p.K = d.f / 2;
   return run_bf16<LAY_K, LAY_K, uint16_t, GRP_M, EPI_STORE, false, GATH_NONE, false, true>(
       p, mtiles_ub(d, MT) * cdiv(d.d, MT), s);
+}
+
+// The INT8 products on 256 x 256 tiles (see gemm_dma_kernel's I8): codes of
+// K (a multiple of 128, at least 512), two to a bf16 slot.
+hipError_t launch_gate_up_i8_tiles(const moe_desc& d, const int32_t* offsets, const int32_t* row_token,
+                                   const int8_t* xq, const float* xs, const int8_t* W1q, const float* W1s,
+                                   const int8_t* W3q, const float* W3s, void* gu, void* h, hipStream_t s) {
+  GemmParams p = blank(d);
+  p.A = xq;
+  p.lda = d.d / 2;
+  p.gather = row_token;
+  p.gather_rows = d.T;
+  p.row_scale = xs;
+  p.B = W1q;
+  p.B2 = W3q;
+  p.bs = W1s;
+  p.bs2 = W3s;
+  p.ldb = d.d / 2;
+  p.b_gstride = (int64_t)d.f * d.d / 2;
+  p.C = h;
+  p.ldc = d.f;
+  p.gu_out = gu;
+  p.offsets = offsets;
+  p.ngroups = d.num_local;
+  p.N = d.f;
+  p.K = d.d / 2;
+  p.c_f32 = 0;
+  return run_i8_tiles<GRP_M, EPI_SWIGLU, true, false, GATH_A>(p, mtiles_ub(d, MT) * cdiv(d.f, MT / 2), s);
+}
+
+hipError_t launch_down_i8_tiles(const moe_desc& d, const int32_t* offsets, const int8_t* hq, const float* hs,
+                                const int8_t* W2q, const float* W2s, void* y_perm, hipStream_t s) {
+  GemmParams p = blank(d);
+  p.A = hq;
+  p.lda = d.f / 2;
+  p.row_scale = hs;
+  p.B = W2q;
+  p.bs = W2s;
+  p.ldb = d.f / 2;
+  p.b_gstride = (int64_t)d.d * d.f / 2;
+  p.C = y_perm;
+  p.ldc = d.d;
+  p.offsets = offsets;
+  p.ngroups = d.num_local;
+  p.N = d.d;
+  p.K = d.f / 2;
+  p.c_f32 = 0;
+  return run_i8_tiles<GRP_M, EPI_STORE, false, false, GATH_NONE>(p, mtiles_ub(d, MT) * cdiv(d.d, MT), s);
+}
+
+hipError_t launch_i8_linear_tiles(int M, int N, int K, const int8_t* xq, int64_t ldx, const float* xs,
+                                  const int8_t* wq, int64_t ldw, const float* ws, const float* bias, void* y,
+                                  int64_t ldy, int dtype, hipStream_t s) {
+  GemmParams p = {};
+  p.A = xq;
+  p.lda = ldx / 2;
+  p.row_scale = xs;
+  p.B = wq;
+  p.bs = ws;
+  p.ldb = ldw / 2;
+  p.bias = bias;
+  p.C = y;
+  p.ldc = ldy;
+  p.ngroups = 1;
+  p.M = M;
+  p.N = N;
+  p.K = K / 2;
+  p.c_f32 = dtype == MOE_F32;
+  const int64_t tiles = cdiv(M, MT) * cdiv(N, MT);
+  if (p.c_f32) return run_i8_tiles<GRP_NONE, EPI_STORE, false, true, GATH_NONE>(p, tiles, s);
+  return run_i8_tiles<GRP_NONE, EPI_STORE, false, false, GATH_NONE>(p, tiles, s);
 }
 
 hipError_t launch_down_q8(const moe_desc& d, const int32_t* offsets, const void* h, const uint8_t* W2q,

@@ -258,8 +258,19 @@ __device__ __forceinline__ void wait_stages(int later) {
 // row (the four blocks k-tile & ~3 .. | 3) into a 2 KB area of the stage,
 // so sbytes is a multiple of 4 (a row's scales padded when K/128 is not).
 // A is read through row_token (GATH_A) or in place (GATH_NONE).
+//
+// I8 (INT8 products): A and B hold int8 codes, two to a bf16 slot as for F8,
+// with one float32 scale per row of A (row_scale; of the source's rows when A
+// is gathered) and per row of B (bs, bs2).  A 16-byte fragment of 8 bf16
+// values is one of 16 codes with the same place in k, so the k-loop is the
+// bf16 one with v_mfma_i32_32x32x32_i8 in place of the bf16 instruction: twice
+// the k per tile and 32-bit integer sums.  The epilogue takes the sums to
+// float32 and applies the row's and the column's scale.  The scales of a
+// tile's 256 rows and columns come by LDS DMA during the tile before it (for
+// a gathered A from its tokens), so the epilogue loads nothing from memory.
+// The host gives it K of at least four k-tiles.
 template <int BK, int STAGES, int ALAY, int BLAY, int GRP, int EPI, bool DUAL, bool CF32, bool DYN, int GATH,
-          bool BQ8, bool F8 = false>
+          bool BQ8, bool F8 = false, bool I8 = false>
 __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
   using namespace dma;
   static_assert(!DUAL || BLAY == LAY_K, "dual B is K-contiguous");
@@ -273,6 +284,9 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
   static_assert(!F8 || (ALAY == LAY_K && BLAY == LAY_K && GRP == GRP_M && !BQ8 &&
                         (GATH == GATH_A || GATH == GATH_NONE)),
                 "FP8 matrix cores: K-contiguous A (in place or read through row_token) and B of GRP_M");
+  static_assert(!I8 || (ALAY == LAY_K && BLAY == LAY_K && !BQ8 && !F8 && (GRP == GRP_M || GRP == GRP_NONE) &&
+                        (GATH == GATH_A || GATH == GATH_NONE) && (EPI == EPI_SWIGLU || EPI == EPI_STORE)),
+                "INT8: K-contiguous A (in place or read through row_token) and B");
   // GKB: the k-rows of an MN-contiguous operand of a grouped-K product are
   // gathered (B for GATH_B, A for GATH_AK), through a ring of token copies.
   constexpr bool GKB = GATH == GATH_B || GATH == GATH_AK;
@@ -296,6 +310,9 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
   // ring position (GATH_B and GATH_AK, eight positions).
   __shared__ __attribute__((aligned(256))) int32_t s_tok[GATH == GATH_A ? 2 : GKB ? 8 : 1]
                                                          [GATH == GATH_A ? 256 : 64];
+
+  // I8: the scales of the rows and columns of this tile and of the next.
+  __shared__ __attribute__((aligned(256))) float s_rsc[I8 ? 2 : 1][I8 ? 256 : 1], s_csc[I8 ? 2 : 1][I8 ? 256 : 1];
 
   Scheduler<GRP, BM, DUAL ? BN / 2 : BN> sched;
   sched.init(p, s_pref, s_scan);
@@ -798,7 +815,9 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
           (P.pfe >= 0 && kp * BK + pr < P.glim ? 0u : 0x80000000u);
   };
 
-  f32x16 acc[MI][NI];
+  typedef int i32x16 __attribute__((ext_vector_type(16)));
+  using Acc = typename std::conditional<I8, i32x16, f32x16>::type;
+  Acc acc[MI][NI];
   // Fragment f (0 .. MI+NI-1) of k-step kk of a ring stage, in the order the
   // MFMAs (mi-major) first use them: A0, B0 .. B3, A1 .. A3.
   // F8 fragment (K-contiguous rows of codes): row row0 + lane%32, the 32
@@ -849,7 +868,7 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
     }
   };
   // The block-scaled product of fragment row MI_ and column NI_ (op_sel must be a constant).
-  auto mfma8 = [&](auto mi_c, auto ni_c, const Frag& a, const Frag& b, f32x16 c) __attribute__((always_inline)) {
+  auto mfma8 = [&](auto mi_c, auto ni_c, const Frag& a, const Frag& b, Acc c) __attribute__((always_inline)) {
     if constexpr (F8)
       return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, decltype(mi_c)::value, (int)sA,
                                                             decltype(ni_c)::value, (int)sB);
@@ -900,8 +919,13 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
         if (!NOREAD && ni == NI - 1) read_frag(rst, rkk, mi == 0 ? 0 : NI + mi, na, nb);
         if (!NOREAD && mi == MI - 1) read_frag(rst, rkk, 1 + ni, na, nb);
       } else {
-        if (mi < MIA && ni < NIA)
-          acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[mi], b[ni], acc[mi][ni], 0, 0, 0);
+        if (mi < MIA && ni < NIA) {
+          if constexpr (I8)
+            acc[mi][ni] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a[mi]),
+                                                                __builtin_bit_cast(i32x4, b[ni]), acc[mi][ni], 0, 0, 0);
+          else
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[mi], b[ni], acc[mi][ni], 0, 0, 0);
+        }
         // (fragment f: a[0], then b[0..NI-1], then a[1..MI-1])
         if ((i & 1) == 0 && (i >> 1) < MI + NI &&
             ((i >> 1) == 0 || ((i >> 1) <= NI ? (i >> 1) - 1 < RNIA : (i >> 1) - NI < RIA)))
@@ -974,7 +998,31 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
   // and whether that has happened.
   Ld lnext = null_ld;
   bool pipe = false, gat_done = true;
-  const int gat_kt = GATH == GATH_A ? __builtin_amdgcn_readfirstlane(p.ngroups >= 0 ? 1 : 2) : -1;
+  const int gat_kt = GATH == GATH_A || I8 ? __builtin_amdgcn_readfirstlane(p.ngroups >= 0 ? 1 : 2) : -1;
+  // I8: the scales of tile q's rows and columns into half `half` of s_rsc and
+  // s_csc; wave w copies entries 64w .. 64w + 63 (past the tile's end: zeros).
+  // With a gathered A the rows' scales are those of its tokens, in `half` of s_tok.
+  auto scale_dma = [&](const TileCtx& q, int half) __attribute__((always_inline)) {
+    const int e = wave * 64 + lane;
+    const bool second = DUAL && wave >= 2;
+    const int c0 = DUAL ? (wave & 1) * 64 : wave * 64;
+    const int nl = DUAL ? min(q.nlim, BN / 2) : q.nlim;
+    const i32x4 rc = make_rsrc((second ? p.bs2 : p.bs) + (GRP == GRP_M ? (int64_t)q.g * p.N : 0) + q.n0, (uint64_t)nl * 4);
+    touch4(rc, (uint32_t)(c0 + lane) * 4u, __builtin_amdgcn_readfirstlane(0u),
+           reinterpret_cast<const uint32_t*>(&s_csc[I8 ? half : 0][I8 ? wave * 64 : 0]));
+    i32x4 rr;
+    uint32_t v = (uint32_t)e * 4u;
+    if (GATH == GATH_A) {
+      rr = make_rsrc(p.row_scale, (uint64_t)p.gather_rows * 4);
+      v = ((uint32_t)s_tok[GATH == GATH_A ? half : 0][GATH == GATH_A ? e : 0] * 4u) | (e < q.mlim ? 0u : 0x80000000u);
+    } else {
+      rr = make_rsrc(p.row_scale + q.m0, (uint64_t)q.mlim * 4);
+    }
+    touch4(rr, v, __builtin_amdgcn_readfirstlane(0u),
+           reinterpret_cast<const uint32_t*>(&s_rsc[I8 ? half : 0][I8 ? wave * 64 : 0]));
+  };
+  TileCtx t_next = t;       // I8: the next tile, if there is one
+  bool t_next_ok = false;
   auto gat_fill_next = [&]() __attribute__((always_inline)) {
     if (!gat_done) {
       tok_fill_tile(lnext, it + 1, gnext, gsn);
@@ -1026,6 +1074,9 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
     // GATH_A: the next tile's tokens (copied at this tile's top, waited for
     // by now in every wave) give its A offsets.
     if (GATH == GATH_A && !FIRST && kt == gat_kt) gat_fill_next();
+    // I8: likewise the next tile's scales (every wave is past the epilogue
+    // that read the half they go to, and their tokens are in LDS).
+    if (I8 && !FIRST && kt == gat_kt && t_next_ok) scale_dma(t_next, (it + 1) & 1);
     const uint16_t* nst = ring[(uint32_t)(gbase + kt + 1) % STAGES];
     if (F8 && !LAST) {  // the scales of position kt+1 (its k-tile index picks the byte)
       int kn;
@@ -1062,6 +1113,11 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
     lds_barrier();
     tok_fill_tile(cur, 0, gcur, gsc);
   }
+  if constexpr (I8) {
+    scale_dma(t, 0);
+    wait_vm<0>();
+    lds_barrier();
+  }
   for (;;) {
     // The next tile of this workgroup, loaded ahead if it is long enough.
     int idn;
@@ -1094,6 +1150,10 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
     // more hands over early.)
     pipe = has_next && lnext.nk >= STAGES && cur.nk >= (GATH != 0 ? 5 : 1);
     nxt = pipe ? lnext : null_ld;
+    if constexpr (I8) {
+      t_next = tn;
+      t_next_ok = has_next;
+    }
     // Half tiles: this tile's A row base, and the next tile's, at which the
     // last k-step reads its first fragments when it is loaded ahead.  (When
     // this tile was loaded ahead, its first fragments were read at the
@@ -1114,7 +1174,7 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
     if (cur.nk > 0) {
       if (!primed) {
@@ -1247,8 +1307,11 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4)
-            stage[((lane_e >> 5) * 4 + r4) * SP + ni * 32 + (lane_e & 31)] = acc[mi_][ni][sl_ * 4 + r4];
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const auto a = acc[mi_][ni][sl_ * 4 + r4];
+            stage[((lane_e >> 5) * 4 + r4) * SP + ni * 32 + (lane_e & 31)] =
+                __builtin_bit_cast(float, a);  // (I8: the whole number's bits)
+          }
       };
       // EPI_SWIGLU_BWD: G and U (ROWSC: and the rows' scales) of slab j = 4 mi
       // + sl into gup[j % 3], issued two slabs before slab j is stored.  Their
@@ -1256,6 +1319,17 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
       // two slabs' time to drain, not those of slab j - 1 (with a batch per
       // 32-row block, each batch waited for the previous block's stores and
       // then made a round trip of its own).
+      // I8: the scales of the lane's W columns (DUAL: of the gate's and of the
+      // up's), the same in every slab.
+      float cs1[I8 ? W : 1], cs2[I8 && DUAL ? W : 1];
+      if constexpr (I8) {
+        const int c = col_base + (lane_e % CPR) * W;
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+          cs1[q] = s_csc[it & 1][c + q];
+          if constexpr (DUAL) cs2[q] = s_csc[it & 1][128 + c + q];
+        }
+      }
       auto load_gu = [&](int j) __attribute__((always_inline)) {
         const int mi_ = j >> 2, sl_ = j & 3;
         const int rowb_ = (HALFM && half) ? (mi_ < 2 ? wm * 64 + mi_ * 32 : 256 + mi_ * 32) : wm * 128 + mi_ * 32;
@@ -1343,6 +1417,14 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
             }
             const int row = rowb + sl * 8 + rl;  // row in the tile
             const int col = col_base + cv;       // column in the tile
+            if constexpr (I8) {
+              const float rs = s_rsc[it & 1][row & 255];  // (an inactive block's rows lie past 255 and are not stored)
+#pragma unroll
+              for (int q = 0; q < W; ++q) {
+                v[q] = (float)__builtin_bit_cast(int, v[q]) * rs * cs1[q];
+                if constexpr (DUAL) v2[q] = (float)__builtin_bit_cast(int, v2[q]) * rs * cs2[q];
+              }
+            }
             const bool ok = col < t.nlim && cv < cvlim;
             const int64_t eo = (int64_t)row * ldo + col;  // element offset from the corner
             if (PLAIN) {

@@ -492,7 +492,10 @@ hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const in
   p.y = h;
   p.ldy = d.f;
   p.gu = reinterpret_cast<uint16_t*>(gu);
-  return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), cdiv((int64_t)d.T * d.k, d.E), s);
+  const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
+  if (d.d % 128 == 0 && d.d >= 512 && mean > 64)
+    return launch_gate_up_i8_tiles(d, offsets, row_token, xq, xs, W1q, W1s, W3q, W3s, gu, h, s);
+  return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), mean, s);
 }
 
 hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_t* hq, const float* hs,
@@ -510,7 +513,10 @@ hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_
   p.K = d.f;
   p.y = y_perm;
   p.ldy = d.d;
-  return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), cdiv((int64_t)d.T * d.k, d.E), s);
+  const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
+  if (d.f % 128 == 0 && d.f >= 512 && mean > 64)
+    return launch_down_i8_tiles(d, offsets, hq, hs, W2q, W2s, y_perm, s);
+  return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), mean, s);
 }
 
 hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, int64_t ldx, const float* xs,
@@ -531,6 +537,10 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
   p.K = (int)K;
   p.y = y;
   p.ldy = ldy;
+  const int64_t esz = dtype == MOE_BF16 ? 2 : 4;
+  if (K % 128 == 0 && K >= 512 && N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 &&
+      cdiv(M, 256) * cdiv(N, 256) >= 128)
+    return launch_i8_linear_tiles((int)M, (int)N, (int)K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, s);
   if (dtype == MOE_BF16) return run_i8<false, uint16_t>(p, M, M, s);
   return run_i8<false, float>(p, M, M, s);
 }

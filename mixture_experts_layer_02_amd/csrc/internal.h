@@ -32,6 +32,14 @@ hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const in
                              const float* W3s, void* gu, void* h, hipStream_t s);
 hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_t* hq, const float* hs,
                           const int8_t* W2q, const float* W2s, void* y_perm, hipStream_t s);
+hipError_t launch_gate_up_i8_tiles(const moe_desc& d, const int32_t* offsets, const int32_t* row_token,
+                                   const int8_t* xq, const float* xs, const int8_t* W1q, const float* W1s,
+                                   const int8_t* W3q, const float* W3s, void* gu, void* h, hipStream_t s);
+hipError_t launch_down_i8_tiles(const moe_desc& d, const int32_t* offsets, const int8_t* hq, const float* hs,
+                                const int8_t* W2q, const float* W2s, void* y_perm, hipStream_t s);
+hipError_t launch_i8_linear_tiles(int M, int N, int K, const int8_t* xq, int64_t ldx, const float* xs,
+                                  const int8_t* wq, int64_t ldw, const float* ws, const float* bias, void* y,
+                                  int64_t ldy, int dtype, hipStream_t s);
 hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, int64_t ldx, const float* xs,
                             const int8_t* wq, int64_t ldw, const float* ws, const float* bias, void* y, int64_t ldy,
                             int dtype, hipStream_t s);
