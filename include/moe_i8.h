@@ -30,7 +30,8 @@ extern "C" {
  *   alone (e.g. offsets + NL: the routed rows of a [R_cap] buffer).  rows may
  *   be 0.  Errors: MOE_ERR_INVALID_ARG for a NULL pointer, w or q not 16-byte
  *   aligned, scale or nrows not 4-byte aligned, or sizes outside these rules;
- *   MOE_ERR_UNSUPPORTED for another dtype. */
+ *   MOE_ERR_UNSUPPORTED for another dtype
+ *   or more than 2^28 cols. */
 int moe_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw,
                          const int32_t* nrows, int8_t* q, int64_t ldq, float* scale, void* stream);
 

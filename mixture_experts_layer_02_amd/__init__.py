@@ -278,28 +278,42 @@ def expert_gate_up_fp8mm(desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, g
     _call("moe_expert_gate_up_fp8mm", desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, gu, h, _stream())
 
 
-def _here(t, name):
-    """The INT8 calls launch on the current device: a tensor of another one is refused."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: a tensor of the current device is needed, not of {t.device}")
-
-
-def _rows(t, name, dtypes):
-    """The distance in elements of the rows of a 2-D tensor (a row's values lie together)."""
-    if t.dim() != 2 or t.dtype not in dtypes:
-        raise ValueError(f"{name}: a 2-D tensor of {' or '.join(str(d) for d in dtypes)} is needed")
-    _here(t, name)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+# The INT8 calls check their tensors, for a wrong one would be read out of
+# range: type, size, layout, and the device, which has to be the current one
+# (they launch there).  A decode step makes many of them, so the checks are few
+# attribute reads each.
+def _rows(t, name, dtype, dev):
+    """Address and distance in elements of the rows of a 2-D tensor (a row's values lie together)."""
+    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev:
+        raise ValueError(f"{name}: a 2-D {dtype} tensor of the current device ({dev}) is needed, "
+                         f"not {t.dim()}-D {t.dtype} of {t.device}")
+    n, m = t.shape
+    ld, one = t.stride()
+    if one != 1 and m > 1:
         raise ValueError(f"{name}: the values of a row must lie together")
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    return t.data_ptr(), ld if n > 1 else (m + 15) // 16 * 16
 
 
-def _flat(t, name, n, dtype):
+def _device(t, name):
+    """The current device, which has to be t's."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor of the current device is needed, not of {t.device}")
+    return dev
+
+
+def _flat(t, name, n, dtype, dev):
     """The address of a contiguous tensor of at least n values."""
-    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor of at least {n} {dtype} is needed")
-    _here(t, name)
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of at least {n} values on the current device ({dev}) "
+                         f"is needed, not {tuple(t.shape)} {t.dtype} of {t.device}")
     return t.data_ptr()
+
+
+def _i8(name, *args):
+    rc = getattr(lib(), name)(*args, _stream())
+    if rc != MOE_OK:
+        raise MoeError(name, rc)
 
 
 def i8_quantize_rows(w, q, scale, nrows=None):
@@ -307,55 +321,54 @@ def i8_quantize_rows(w, q, scale, nrows=None):
     code = 127 w / max|row| (ties to even), scale = max|row| / 127.  Rows of w
     and q may lie apart (q's by a multiple of 16); rows at or past the device
     int32 nrows (if given) are left alone."""
-    ldw = _rows(w, "w", (torch.bfloat16, torch.float32))
-    ldq = _rows(q, "q", (torch.int8,))
+    dev = _device(w, "w")
+    bf = w.dtype is torch.bfloat16
+    wp, ldw = _rows(w, "w", torch.bfloat16 if bf else torch.float32, dev)
+    qp, ldq = _rows(q, "q", torch.int8, dev)
     rows, cols = w.shape
     if q.shape != w.shape:
         raise ValueError("q must have w's shape")
-    if rows == 0:
-        return
-    rc = lib().moe_i8_quantize_rows(w.data_ptr(), MOE_BF16 if w.dtype == torch.bfloat16 else MOE_F32, rows, cols, ldw,
-                                    None if nrows is None else _flat(nrows, "nrows", 1, torch.int32), q.data_ptr(),
-                                    ldq, _flat(scale, "scale", rows, torch.float32), _stream())
-    if rc != MOE_OK:
-        raise MoeError("moe_i8_quantize_rows", rc)
+    if rows:
+        _i8("moe_i8_quantize_rows", wp, MOE_BF16 if bf else MOE_F32, rows, cols, ldw,
+            None if nrows is None else _flat(nrows, "nrows", 1, torch.int32, dev), qp, ldq,
+            _flat(scale, "scale", rows, torch.float32, dev))
 
 
 def i8_linear(xq, xs, wq, ws, y, bias=None):
     """y [M][N] (bf16 or fp32) = xs ws (xq wq^T) + bias from codes xq [M][K],
     wq [N][K] (rows apart by multiples of 16) and float32 scales xs [M], ws [N]."""
-    ldx, ldw = _rows(xq, "xq", (torch.int8,)), _rows(wq, "wq", (torch.int8,))
-    ldy = _rows(y, "y", (torch.bfloat16, torch.float32))
+    dev = _device(y, "y")
+    bf = y.dtype is torch.bfloat16
+    xp, ldx = _rows(xq, "xq", torch.int8, dev)
+    wp, ldw = _rows(wq, "wq", torch.int8, dev)
+    yp, ldy = _rows(y, "y", torch.bfloat16 if bf else torch.float32, dev)
     (M, K), N = xq.shape, wq.shape[0]
     if wq.shape[1] != K or y.shape != (M, N):
         raise ValueError("xq [M][K], wq [N][K] and y [M][N] do not fit")
-    if M == 0:
-        return
-    rc = lib().moe_i8_linear(M, N, K, xq.data_ptr(), ldx, _flat(xs, "xs", M, torch.float32), wq.data_ptr(), ldw,
-                             _flat(ws, "ws", N, torch.float32), None if bias is None else _flat(bias, "bias", N, torch.float32), y.data_ptr(),
-                             ldy, MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, _stream())
-    if rc != MOE_OK:
-        raise MoeError("moe_i8_linear", rc)
+    if M:
+        f32 = torch.float32
+        _i8("moe_i8_linear", M, N, K, xp, ldx, _flat(xs, "xs", M, f32, dev), wp, ldw, _flat(ws, "ws", N, f32, dev),
+            None if bias is None else _flat(bias, "bias", N, f32, dev), yp, ldy, MOE_BF16 if bf else MOE_F32)
 
 
 def expert_gate_up_i8(desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, gu, h):
     """gate/up + SwiGLU on INT8 codes with a scale per token and per channel."""
     T, d, f, NL, Rc = desc.T, desc.d, desc.f, desc.num_local, desc.R_cap
-    i8, f32, bf = torch.int8, torch.float32, torch.bfloat16
-    _call("moe_expert_gate_up_i8", desc, _flat(offsets, "offsets", NL + 1, torch.int32),
-          _flat(row_token, "row_token", Rc, torch.int32), _flat(xq, "xq", T * d, i8), _flat(xs, "xs", T, f32),
-          _flat(w1q, "w1q", NL * f * d, i8), _flat(w1s, "w1s", NL * f, f32), _flat(w3q, "w3q", NL * f * d, i8),
-          _flat(w3s, "w3s", NL * f, f32), None if gu is None else _flat(gu, "gu", Rc * 2 * f, bf),
-          _flat(h, "h", Rc * f, bf), _stream())
+    i8, f32, i32, bf, dev = torch.int8, torch.float32, torch.int32, torch.bfloat16, _device(h, "h")
+    _i8("moe_expert_gate_up_i8", ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, i32, dev),
+        _flat(row_token, "row_token", Rc, i32, dev), _flat(xq, "xq", T * d, i8, dev), _flat(xs, "xs", T, f32, dev),
+        _flat(w1q, "w1q", NL * f * d, i8, dev), _flat(w1s, "w1s", NL * f, f32, dev),
+        _flat(w3q, "w3q", NL * f * d, i8, dev), _flat(w3s, "w3s", NL * f, f32, dev),
+        None if gu is None else _flat(gu, "gu", Rc * 2 * f, bf, dev), _flat(h, "h", Rc * f, bf, dev))
 
 
 def expert_down_i8(desc, offsets, hq, hs, w2q, w2s, y_perm):
     """down on INT8 codes with a scale per row and per channel."""
     d, f, NL, Rc = desc.d, desc.f, desc.num_local, desc.R_cap
-    _call("moe_expert_down_i8", desc, _flat(offsets, "offsets", NL + 1, torch.int32),
-          _flat(hq, "hq", Rc * f, torch.int8), _flat(hs, "hs", Rc, torch.float32),
-          _flat(w2q, "w2q", NL * d * f, torch.int8), _flat(w2s, "w2s", NL * d, torch.float32),
-          _flat(y_perm, "y_perm", Rc * d, torch.bfloat16), _stream())
+    i8, f32, dev = torch.int8, torch.float32, _device(y_perm, "y_perm")
+    _i8("moe_expert_down_i8", ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, torch.int32, dev),
+        _flat(hq, "hq", Rc * f, i8, dev), _flat(hs, "hs", Rc, f32, dev), _flat(w2q, "w2q", NL * d * f, i8, dev),
+        _flat(w2s, "w2s", NL * d, f32, dev), _flat(y_perm, "y_perm", Rc * d, torch.bfloat16, dev))
 
 
 def fp8_dequantize(q, scales, w):

@@ -448,7 +448,7 @@ int moe_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64_t cols, i
   if (!need(w) || !need(q) || !scale || (reinterpret_cast<uintptr_t>(scale) & 3u) ||
       (reinterpret_cast<uintptr_t>(nrows) & 3u) || rows < 0 || cols < 1 || ldw < cols || ldq < cols || ldq % 16)
     return MOE_ERR_INVALID_ARG;
-  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if ((dtype != MOE_BF16 && dtype != MOE_F32) || cols > 1 << 28) return MOE_ERR_UNSUPPORTED;
   return finish(moe::launch_i8_quantize_rows(w, dtype, rows, cols, ldw, nrows, q, ldq, scale, S(stream)));
 }
 

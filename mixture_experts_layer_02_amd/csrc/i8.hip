@@ -22,6 +22,8 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // ---------------------------------------------------------------------------
 // Row quantiser
 // ---------------------------------------------------------------------------
@@ -46,17 +48,17 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 // A row's quantisation from its largest |value| (as bits, so that NaN > inf >
-// every number).  code(v) is 127 v / max rounded to nearest, ties to even,
-// exactly: r = v (127 / max) is off by at most 2^-23 of itself, so rint(r) is
-// right unless r lies about that near to a tie (10^-6 of itself is asked).
-// There, for float values, the quotient is taken in 64 bits, where none is
-// nearer than 2^-40 of itself to a tie without being one.  For bf16 values, of
-// 8 bits each, 254 v = (2n + 1) max is an equation of whole numbers up to
-// 255^2 and a power of two, so none is nearer than 1.5 10^-5 of itself: what r
-// cannot tell from a tie is one (v = max / 2 is: 63.5), and the even
-// neighbour is 2 rint(r / 2).  A row of zeros has scale 0; a row with an
-// infinity or a NaN has scale NaN and codes 0, so that what is computed from
-// it is NaN.
+// every number).  The codes are 127 v / max rounded to nearest, ties to even,
+// exactly: r = v (127 / max) is off by at most 2^-23 of itself, so the integer
+// nearest to r is right unless r lies about that near to a tie (the slow form;
+// 2 10^-4 is asked, for |r| up to 127).  There, for float values, the quotient is taken
+// in 64 bits, where none is nearer than 2^-40 of itself to a tie without being
+// one.  For bf16 values, of 8 bits each, 254 v = (2n + 1) max is an equation of
+// whole numbers up to 255^2 and a power of two, so none is nearer than 1.5 10^-5
+// of itself: what lies within 10^-6 of itself is a tie (v = max / 2 is: 63.5),
+// and the even neighbour is 2 rint(r / 2).  A row of zeros has scale 0; a row
+// with an infinity or a NaN has scale NaN and codes 0, so that what is computed
+// from it is NaN.
 struct RowQuant {
   float top, inv;
   bool small;  // 127 / max overflows: every quotient in 64 bits
@@ -65,123 +67,164 @@ struct RowQuant {
     top = __uint_as_float(bits);
     none = bits == 0 || bits >= 0x7f800000u;
     small = !none && top < 0x1p-100f;
-    inv = none ? 0.f : 127.0f / top;
+    inv = none || small ? 0.f : 127.0f / top;
   }
   __device__ __forceinline__ float scale() const {
     return none && __float_as_uint(top) ? __uint_as_float(0x7fc00000u) : top / 127.0f;
   }
-  template <bool EXACT>
-  __device__ __forceinline__ int code(float v) const {
-    const float r = v * inv;
-    int q = (int)rintf(r);
-    const bool tie = fabsf(fabsf(r - truncf(r)) - 0.5f) < 1e-6f * fabsf(r);
-    if (!EXACT && tie) q = 2 * (int)rintf(r * 0.5f);
-    if (EXACT && tie) q = (int)rint((double)v * 127.0 / (double)top);
-    if (small) q = (int)rint((double)v * 127.0 / (double)top);
-    return none ? 0 : q;
+  // N codes, four to a dword.  r + 1.5 2^23 rounds r to the nearest integer,
+  // ties to even, in the low bits of its own bit pattern.
+  template <bool EXACT, int N>
+  __device__ __forceinline__ void codes(const float (&v)[N], uint32_t (&o)[(N + 3) / 4]) const {
+    constexpr float MAGIC = 12582912.0f;
+    uint32_t b[N];
+    float off = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float r = none ? 0.f : v[i] * inv;
+      const float m = r + MAGIC;
+      b[i] = __float_as_uint(m);
+      off = fmaxf(off, fabsf(r - (m - MAGIC)));
+    }
+    if (off > 0.4998f || small) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float r = v[i] * inv;
+        const bool tie = fabsf(fabsf(r - truncf(r)) - 0.5f) < 1e-6f * fabsf(r);
+        int q = (int)rintf(r);
+        if (EXACT ? tie || small : small) q = (int)rint((double)v[i] * 127.0 / (double)top);
+        else if (tie) q = 2 * (int)rintf(r * 0.5f);
+        b[i] = (uint32_t)q;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < (N + 3) / 4; ++j) {
+      o[j] = 0;
+#pragma unroll
+      for (int i = 4 * j; i < N && i < 4 * j + 4; ++i) o[j] |= (b[i] & 0xffu) << (8 * (i - 4 * j));
+    }
   }
 };
 
-// One wave per row.  NV > 0: the row is held in NV vectors per lane and read
+// W waves per row.  NV > 0: the row is held in NV vectors per lane and read
 // once; NV = 0: any length, read twice (the second time from cache).  VEC:
-// rows start at multiples of 16 bytes, so the values come as vectors (the last
-// may reach past the row's end, never past the 16 aligned bytes that hold its
-// last value).  nrows (device, or NULL): rows at or past it are left alone.
-// Bound by HBM: (b + 1) bytes a value.
-template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(256) i8_quant_rows_kernel(const T* __restrict__ w, int64_t rows, int64_t cols,
+// rows start at multiples of 16 bytes, so values and codes go as vectors,
+// through buffer resources that end with the row (loads past it give zeros,
+// stores past it are dropped, each by whole 4 bytes).  nrows (device, or NULL):
+// rows at or past it are left alone.
+// Bound by HBM, (b + 1) bytes a value; with few rows by one row's latency,
+// hence four waves on it.
+template <typename T, int W, int NV, bool VEC>
+__global__ void __launch_bounds__(256) i8_quant_rows_kernel(const T* __restrict__ w, int64_t rows, int cols,
                                                             int64_t ldw, const int32_t* __restrict__ nrows,
                                                             int8_t* __restrict__ q, int64_t ldq,
                                                             float* __restrict__ scale) {
-  constexpr int N = 16 / sizeof(T);
+  constexpr int N = VEC ? 16 / sizeof(T) : 1;  // values per load
+  constexpr int L = W * 64;                    // lanes per row
   constexpr bool EXACT = sizeof(T) == 4;
-  const int lane = threadIdx.x & 63;
+  __shared__ uint32_t s_top[4];
+  const int sub = threadIdx.x % L;
+  const int rw = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   const int64_t lim = nrows ? min(rows, (int64_t)max(*nrows, 0)) : rows;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < lim; r += (int64_t)gridDim.x * 4) {
-    const T* src = w + r * ldw;
+  for (int64_t r = (int64_t)blockIdx.x * (4 / W) + rw; r < lim; r += (int64_t)gridDim.x * (4 / W)) {
+    T* src = const_cast<T*>(w) + r * ldw;
     int8_t* dst = q + r * ldq;
-    if constexpr (VEC) {
-      u32x4_t held[NV > 0 ? NV : 1];
-      uint32_t top = 0;
-      auto load = [&](int64_t c) -> u32x4_t {  // columns c .. c + N - 1, zero past the end
-        u32x4_t x = {0, 0, 0, 0};
-        if (c < cols) x = *reinterpret_cast<const u32x4_t*>(src + c);
-        if (c + N > cols) {
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(src, (short)0, (int)((cols * sizeof(T) + 3) & ~3u), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rd = __builtin_amdgcn_make_buffer_rsrc(dst, (short)0, cols & ~3, 0x00020000);
+    // The N values of column c and on, as they lie in memory.
+    using Raw = typename std::conditional<VEC, u32x4_t, float>::type;
+    auto load = [&](int c) -> Raw {
+      if constexpr (VEC) {
+        u32x4_t x = __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)c * (uint32_t)sizeof(T), 0, 0);
+        if (sizeof(T) == 2 && (cols & 1) && c < cols && c + N > cols) {  // half of the row's last 4 bytes is not its own
+          const int d = (cols - c) >> 1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (sizeof(T) == 4) {
-              if (c + i >= cols) x[i] = 0;
-            } else {
-              if (c + 2 * i >= cols) x[i] = 0;
-              else if (c + 2 * i + 1 >= cols) x[i] &= 0xffffu;
-            }
-          }
+          for (int i = 0; i < 4; ++i) x[i] &= i == d ? 0xffffu : 0xffffffffu;
         }
         return x;
-      };
-      auto grow = [&](u32x4_t x) {
-        float v[N];
-        unpack(x, v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-      };
-      if constexpr (NV > 0) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) held[j] = load((int64_t)(j * 64 + lane) * N);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) grow(held[j]);
       } else {
-        for (int64_t c = (int64_t)lane * N; c < cols; c += 64 * N) grow(load(c));
+        return Elem<T>::ld(src, c);
       }
-      const RowQuant rq(wave_max(top));
-      auto put = [&](int64_t c, u32x4_t x) {
-        if (c >= cols) return;
-        float v[N];
-        unpack(x, v);
-        uint32_t o[N / 4];
+    };
+    auto wide = [&](const Raw& x, float (&v)[N]) {
+      if constexpr (VEC) unpack(x, v);
+      else v[0] = x;
+    };
+    uint32_t top = 0;
+    auto grow = [&](const Raw& x) {
+      float v[N];
+      wide(x, v);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const uint32_t b = (uint32_t)rq.template code<EXACT>(v[i]) & 0xffu;
-          o[i / 4] = i % 4 ? o[i / 4] | (b << (8 * (i % 4))) : b;
-        }
-        if (c + N <= cols) {
-          if constexpr (N == 8) *reinterpret_cast<u32x2_t*>(dst + c) = u32x2_t{o[0], o[1]};
-          else *reinterpret_cast<uint32_t*>(dst + c) = o[0];
-        } else {
-          for (int i = 0; c + i < cols; ++i) dst[c + i] = (int8_t)(o[i / 4] >> (8 * (i % 4)));
-        }
-      };
-      if constexpr (NV > 0) {
+      for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    };
+    Raw held[NV > 0 ? NV : 1];
+    if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) put((int64_t)(j * 64 + lane) * N, held[j]);
-      } else {
-        for (int64_t c = (int64_t)lane * N; c < cols; c += 64 * N) put(c, load(c));
-      }
-      if (lane == 0) scale[r] = rq.scale();
+      for (int j = 0; j < NV; ++j) held[j] = load((j * L + sub) * N);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) grow(held[j]);
     } else {
-      uint32_t top = 0;
-      for (int64_t c = lane; c < cols; c += 64)
-        top = max(top, __float_as_uint(Elem<T>::ld(src, c)) & 0x7fffffffu);
-      const RowQuant rq(wave_max(top));
-      for (int64_t c = lane; c < cols; c += 64) dst[c] = (int8_t)rq.template code<EXACT>(Elem<T>::ld(src, c));
-      if (lane == 0) scale[r] = rq.scale();
+      for (int c = sub * N; c < cols; c += L * N) grow(load(c));
     }
+    top = wave_max(top);
+    if constexpr (W > 1) {  // (every wave of the workgroup has the same row)
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < W; ++i) top = max(top, s_top[i]);
+    }
+    const RowQuant rq(top);
+    auto put = [&](int c, const Raw& x) {
+      float v[N];
+      wide(x, v);
+      uint32_t o[(N + 3) / 4];
+      rq.template codes<EXACT, N>(v, o);
+      if constexpr (!VEC) {
+        dst[c] = (int8_t)o[0];
+      } else {
+        if constexpr (N == 8) __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{o[0], o[1]}, rd, (uint32_t)c, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(o[0], rd, (uint32_t)c, 0, 0);
+        if ((cols & 3) && c < cols && c + N > (cols & ~3)) {  // the row's last one to three codes
+          const int z = cols & ~3;
+          for (int i = z; i < cols; ++i) dst[i] = (int8_t)(o[(z - c) / 4] >> (8 * (i - z)));
+        }
+      }
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if constexpr (VEC) asm volatile("" : "+v"(held[j]));  // widened again, not kept as float
+        put((j * L + sub) * N, held[j]);
+      }
+    } else {
+      for (int c = sub * N; c < cols; c += L * N) put(c, load(c));
+    }
+    if (sub == 0) scale[r] = rq.scale();
   }
 }
 
 template <typename T>
-hipError_t quant_rows(const T* w, int64_t rows, int64_t cols, int64_t ldw, const int32_t* nrows, int8_t* q,
+hipError_t quant_rows(const T* w, int64_t rows, int cols, int64_t ldw, const int32_t* nrows, int8_t* q,
                       int64_t ldq, float* scale, hipStream_t s) {
   constexpr int64_t N = 16 / sizeof(T);
-  const int64_t nv = (cols + 64 * N - 1) / (64 * N);  // vectors per lane
-  const unsigned grid = (unsigned)std::min<int64_t>((rows + 3) / 4, (int64_t)num_cus() * 16);
-#define MOE_I8_QUANT(NV, VEC) \
-  i8_quant_rows_kernel<T, NV, VEC><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale)
-  if (ldw % N) MOE_I8_QUANT(0, false);
-  else if (nv <= 4) MOE_I8_QUANT(4, true);
-  else if (nv <= 12) MOE_I8_QUANT(12, true);
-  else MOE_I8_QUANT(0, true);
-#undef MOE_I8_QUANT
+  const int64_t nv = cdiv(cols, 64 * N);  // vectors per lane of one wave
+  const int64_t cap = (int64_t)num_cus() * 16;
+  const bool vec = ldw % N == 0;
+  // A wave per row needs a few rows per CU and a row it can hold.
+  if (vec && nv <= 12 && rows >= (int64_t)num_cus() * 8) {
+    const unsigned grid = (unsigned)std::min(cdiv(rows, 4), cap);
+    if (nv <= 4)
+      i8_quant_rows_kernel<T, 1, 4, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
+    else
+      i8_quant_rows_kernel<T, 1, 12, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
+    return hipGetLastError();
+  }
+  const unsigned grid = (unsigned)std::min(rows, cap);
+  if (!vec) i8_quant_rows_kernel<T, 4, 0, false><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
+  else if (nv <= 12) i8_quant_rows_kernel<T, 4, 3, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
+  else i8_quant_rows_kernel<T, 4, 0, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
   return hipGetLastError();
 }
 
@@ -214,22 +257,114 @@ struct I8Params {
   uint16_t* gu;
 };
 
+// The group and the rows [m0, m0 + mlim) of m-tile `slot`: groups have
+// ceil(rows / MT) m-tiles each, in order.  Every wave searches alike, 64 groups
+// at a time.  False past the last m-tile.
+template <int MT>
+__device__ __forceinline__ bool find_tile(const I8Params& p, int slot, int lane, int& g, int& m0, int& mlim) {
+  g = 0;
+  m0 = slot * MT;
+  int m1 = p.M;
+  if (p.offsets) {
+    int before = 0;
+    g = -1;
+    for (int base = 0; base < p.ngroups; base += 64) {
+      const int i = base + lane;
+      const int lo = i < p.ngroups ? p.offsets[i] : 0, hi = i < p.ngroups ? p.offsets[i + 1] : 0;
+      const int c = (hi - lo + MT - 1) / MT;
+      int inc = c;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(inc, o, WAVE);
+        if (lane >= o) inc += v;
+      }
+      const unsigned long long past = __ballot(before + inc > slot);
+      if (past) {
+        const int l = __ffsll(past) - 1;
+        g = base + l;
+        m0 = __shfl(lo, l, WAVE) + (slot - before - (__shfl(inc, l, WAVE) - __shfl(c, l, WAVE))) * MT;
+        m1 = __shfl(hi, l, WAVE);
+        break;
+      }
+      before += __shfl(inc, 63, WAVE);
+    }
+  }
+  g = __builtin_amdgcn_readfirstlane(g);
+  m0 = __builtin_amdgcn_readfirstlane(m0);
+  mlim = __builtin_amdgcn_readfirstlane(min(MT, m1 - m0));
+  return g >= 0;
+}
+
+// The outputs of one row r and the four channels n .. n + 3 of group g (n a
+// multiple of 4) from their sums: s1 alone, or gate s1 and up s2.
+template <bool DUAL, typename OUT>
+__device__ __forceinline__ void store4(const I8Params& p, int g, int64_t r, int n, float sx, i32x4_t s1, i32x4_t s2) {
+  float o[4];
+  const int64_t ch = (int64_t)g * p.N + n;
+  if constexpr (DUAL) {
+    float gt[4], up[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // (N is a multiple of 64)
+      gt[q] = (float)s1[q] * sx * p.sw[ch + q];
+      up[q] = (float)s2[q] * sx * p.sw2[ch + q];
+      o[q] = gt[q] * sigmoidf_(gt[q]) * up[q];
+    }
+    if (p.gu) {
+      uint16_t* gr = p.gu + r * 2 * p.N + n;
+      *reinterpret_cast<u32x2_t*>(gr) = u32x2_t{pack_bf2(gt[0], gt[1]), pack_bf2(gt[2], gt[3])};
+      *reinterpret_cast<u32x2_t*>(gr + p.N) = u32x2_t{pack_bf2(up[0], up[1]), pack_bf2(up[2], up[3])};
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (n + q >= p.N) break;
+      o[q] = (float)s1[q] * sx * p.sw[ch + q];
+      if (p.bias) o[q] += p.bias[ch + q];
+    }
+  }
+  OUT* y = reinterpret_cast<OUT*>(p.y) + r * p.ldy + n;
+  if (p.N % 4 == 0 && p.ldy % 4 == 0) {  // (then the four are inside and their address is aligned)
+    if constexpr (sizeof(OUT) == 2)
+      *reinterpret_cast<u32x2_t*>(y) = u32x2_t{pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3])};
+    else *reinterpret_cast<f32x4_t*>(y) = f32x4_t{o[0], o[1], o[2], o[3]};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < p.N) Elem<OUT>::st(y, q, o[q]);
+  }
+}
+
+// Zeroes the codes at k >= K of a fragment whose lane holds 16 codes from k on.
+__device__ __forceinline__ i32x4_t mask_k(i32x4_t f, int left) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int v = left - 4 * d;
+    f[d] &= v >= 4 ? -1 : v <= 0 ? 0 : (int)((1u << (8 * v)) - 1u);
+  }
+  return f;
+}
+
 // With few rows the product streams the weights, each of whose bytes is used
 // by one workgroup only: the kernel is bound by HBM and has to keep many loads
 // in flight.  A workgroup computes MB*16 rows x NB*16 channels (DUAL: half of
 // them gate, half up) over all of K, cut into chunks of 128 codes that its
 // four waves take in turn; no wave shares an operand with another, so the main
-// loop has no barrier: each wave copies its own chunks into its own LDS ring
-// (LDS DMA, 8 rows x 128 bytes per instruction, all lines whole) and waits for
-// its own copies only.  The four partial sums are whole numbers and are added
-// through LDS at the end, in any order with the same result.
+// loop has no barrier: each wave copies a chunk into its own part of LDS (LDS
+// DMA, 8 rows x 128 bytes per instruction, all lines whole), waits for it,
+// takes it to registers, starts the next copy over it and multiplies.  Several
+// workgroups share a CU (WGS at least), so a CU's whole LDS is in flight most of
+// the time.  (Measured on gate/up, d = 6144, f = 1792, 96 experts of which 21
+// rows each: 372 us, 5.7 TB/s; a ring of two stages with half the workgroups
+// took 512 us, chunks of 64 codes, half lines, 451 us.)  The four partial sums
+// are whole numbers and are added through LDS at the end, in any order with the
+// same result.
 //   Fragments: v_mfma_i32_16x16x64_i8 with the channels as rows and the tokens
 //   as columns; lane l holds 16 codes of row l % 16 at k = 16 (l / 16), and
 //   the result's rows 4 (l / 16) .. + 3 of column l % 16, so a lane's four
 //   sums are consecutive channels of one token.
 //   LDS: rows of 128 bytes, 16-byte piece c of row r at c ^ swz_k(r).
-template <int MB, int NB, int NST, bool DUAL, typename OUT>
-__global__ void __launch_bounds__(256) i8_few_rows_kernel(I8Params p) {
+template <int MB, int NB, int WGS, bool DUAL, typename OUT>
+__global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
   using namespace dma;
   static_assert(!DUAL || NB % 2 == 0, "gate and up blocks");
   constexpr int MT = MB * 16, NT = NB * 16;
@@ -237,8 +372,7 @@ __global__ void __launch_bounds__(256) i8_few_rows_kernel(I8Params p) {
   constexpr int STAGE = (MT + NT) * 128;       // bytes: weight rows, then token rows
   constexpr int PER = (MT + NT) / 8;           // copies per chunk
   constexpr int RP = NT + 4;                   // pitch of the partial sums (ints)
-  constexpr int RING = 4 * NST * STAGE, RED = 4 * MT * RP * 4;
-  static_assert(PER * (NST - 1) < 64, "vmcnt range");
+  constexpr int RING = 4 * STAGE, RED = 4 * MT * RP * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > RED ? RING : RED];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -248,38 +382,8 @@ __global__ void __launch_bounds__(256) i8_few_rows_kernel(I8Params p) {
     const int ntile = (int)(id % ntiles);
     const int slot = (int)(id / ntiles);
 
-    // The slot's group and m-tile: groups have ceil(rows / MT) m-tiles each, in
-    // order.  Every wave searches alike, 64 groups at a time.
-    int g = 0, m0 = slot * MT, m1 = p.M;
-    if (p.offsets) {
-      int before = 0;
-      g = -1;
-      for (int base = 0; base < p.ngroups; base += 64) {
-        const int i = base + lane;
-        const int lo = i < p.ngroups ? p.offsets[i] : 0, hi = i < p.ngroups ? p.offsets[i + 1] : 0;
-        const int c = (hi - lo + MT - 1) / MT;
-        int inc = c;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const int v = __shfl_up(inc, o, WAVE);
-          if (lane >= o) inc += v;
-        }
-        const unsigned long long past = __ballot(before + inc > slot);
-        if (past) {
-          const int l = __ffsll(past) - 1;
-          g = base + l;
-          const int mt = slot - before - (__shfl(inc, l, WAVE) - __shfl(c, l, WAVE));
-          m0 = __shfl(lo, l, WAVE) + mt * MT;
-          m1 = __shfl(hi, l, WAVE);
-          break;
-        }
-        before += __shfl(inc, 63, WAVE);
-      }
-      if (g < 0) break;  // more slots than m-tiles (and every later slot is past them too)
-    }
-    g = __builtin_amdgcn_readfirstlane(g);
-    m0 = __builtin_amdgcn_readfirstlane(m0);
-    const int mlim = __builtin_amdgcn_readfirstlane(min(MT, m1 - m0));
+    int g, m0, mlim;
+    if (!find_tile<MT>(p, slot, lane, g, m0, mlim)) break;  // (every later slot is past the last m-tile too)
     const int n0 = ntile * OC, nlim = min(OC, p.N - n0);
 
     // Copy offsets.  Copy j moves LDS rows 8j .. 8j + 7: lane i row 8j + i/8,
@@ -306,19 +410,21 @@ __global__ void __launch_bounds__(256) i8_few_rows_kernel(I8Params p) {
 
     const int chunks = (p.K + 127) / 128;
     const int mine = (chunks - wave + 3) / 4;  // chunks wave, wave + 4, ...
-    const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * NST * STAGE;
-    auto copy = [&](int i) {  // the wave's chunk i into stage i % NST
-      const int k0 = (wave + 4 * i) * 128;
-      const uint32_t st = ring + (i % NST) * STAGE;
+    const uint32_t st_lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * STAGE;
+    const uint8_t* st = smem + wave * STAGE;
+    auto k_of = [&](int i) { return (wave + 4 * i) * 128; };
+    auto copy = [&](int i) {
+      const int k0 = k_of(i);
       const bool whole = k0 + 128 <= p.K;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const bool tok = j >= NT / 8;
-        uint32_t v = tok ? vx[tok ? j - NT / 8 : 0] : vw[tok ? 0 : j];
+        const int jj = tok ? j - NT / 8 : j;
+        uint32_t v = tok ? vx[tok ? jj : 0] : vw[tok ? 0 : jj];
         // (a piece past K lies in the next row: none of it is wanted)
-        if (!whole && k0 + piece(8 * (tok ? j - NT / 8 : j) + (lane >> 3)) * 16 >= p.K) v = 0x80000000u;
+        if (!whole && k0 + piece(8 * jj + (lane >> 3)) * 16 >= p.K) v = 0x80000000u;
         const i32x4 r = tok ? rx : (DUAL && j >= NT / 16 ? rw2 : rw);
-        dma16(r, v, (uint32_t)k0, __builtin_amdgcn_readfirstlane(st + j * 1024));
+        dma16(r, v, (uint32_t)k0, __builtin_amdgcn_readfirstlane(st_lds + j * 1024));
       }
     };
 
@@ -328,47 +434,37 @@ __global__ void __launch_bounds__(256) i8_few_rows_kernel(I8Params p) {
 #pragma unroll
       for (int b = 0; b < MB; ++b) acc[a][b] = i32x4_t{0, 0, 0, 0};
 
-#pragma unroll
-    for (int i = 0; i < NST; ++i)
-      if (i < mine) copy(i);
+    if (mine > 0) copy(0);
     for (int i = 0; i < mine; ++i) {
-      wait_stages<PER, NST - 1>(min(NST - 1, mine - 1 - i));
+      wait_vm<0>();
       asm volatile("" ::: "memory");
-      const uint8_t* st = smem + (wave * NST + i % NST) * STAGE;
       i32x4_t fw[2][NB], fx[2][MB];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
           const int r = b * 16 + (lane & 15);
-          fx[ks][b] = *reinterpret_cast<const i32x4_t*>(st + NT * 128 + r * 128 +
-                                                        (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+          fx[ks][b] = *reinterpret_cast<const i32x4_t*>(st + (NT + r) * 128 +
+                                                         (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
         }
 #pragma unroll
         for (int a = 0; a < NB; ++a) {
           const int r = a * 16 + (lane & 15);
-          fw[ks][a] =
-              *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+          fw[ks][a] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
         }
       }
-      // The stage is read before its next copy is issued.
+      // The chunk is in registers before the next one is copied over it.
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       asm volatile("" ::: "memory");
-      if (i + NST < mine) copy(i + NST);
-      if ((wave + 4 * i) * 128 + 128 > p.K && p.K % 16) {
+      if (i + 1 < mine) copy(i + 1);
+      const int k0 = k_of(i);
+      if (k0 + 128 > p.K && p.K % 16) {
         // the codes past K in the row's last piece are not the caller's to give:
         // zeroed in one operand, the other's do not matter
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const int left = p.K - ((wave + 4 * i) * 128 + ks * 64 + (lane >> 4) * 16);  // valid codes of the lane's 16
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int v = left - 4 * d;
-            const uint32_t keep = v >= 4 ? 0xffffffffu : v <= 0 ? 0u : (1u << (8 * v)) - 1u;
-#pragma unroll
-            for (int b = 0; b < MB; ++b) fx[ks][b][d] &= (int)keep;
-          }
-        }
+          for (int b = 0; b < MB; ++b) fx[ks][b] = mask_k(fx[ks][b], p.K - (k0 + ks * 64 + (lane >> 4) * 16));
       }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
@@ -395,70 +491,193 @@ __global__ void __launch_bounds__(256) i8_few_rows_kernel(I8Params p) {
       return v;
     };
     constexpr int VPR = OC / 4;  // vectors of four channels per row
-    const bool vec = p.N % 4 == 0 && p.ldy % 4 == 0;  // (then a vector is whole or outside, and aligned)
     for (int e = tid; e < mlim * VPR; e += 256) {
       const int row = e / VPR, c = (e % VPR) * 4;
       if (c >= nlim) continue;
       const int64_t r = (int64_t)m0 + row;
-      const float sx = p.sx[p.row_token ? p.row_token[r] : r];
       const i32x4_t s1 = total(row, c);
-      float o[4];
-      const int64_t ch = (int64_t)g * p.N + n0 + c;
-      if constexpr (DUAL) {
-        const i32x4_t s2 = total(row, OC + c);
-        float gt[4], up[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // (N is a multiple of 64)
-          gt[q] = (float)s1[q] * sx * p.sw[ch + q];
-          up[q] = (float)s2[q] * sx * p.sw2[ch + q];
-          o[q] = gt[q] * sigmoidf_(gt[q]) * up[q];
-        }
-        if (p.gu) {
-          uint16_t* gr = p.gu + r * 2 * p.N + n0 + c;
-          *reinterpret_cast<u32x2_t*>(gr) = u32x2_t{pack_bf2(gt[0], gt[1]), pack_bf2(gt[2], gt[3])};
-          *reinterpret_cast<u32x2_t*>(gr + p.N) = u32x2_t{pack_bf2(up[0], up[1]), pack_bf2(up[2], up[3])};
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (c + q >= nlim) break;
-          o[q] = (float)s1[q] * sx * p.sw[ch + q];
-          if (p.bias) o[q] += p.bias[ch + q];
-        }
-      }
-      OUT* y = reinterpret_cast<OUT*>(p.y) + r * p.ldy + n0 + c;
-      if (vec) {
-        if constexpr (sizeof(OUT) == 2)
-          *reinterpret_cast<u32x2_t*>(y) = u32x2_t{pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3])};
-        else *reinterpret_cast<f32x4_t*>(y) = f32x4_t{o[0], o[1], o[2], o[3]};
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c + q < nlim) Elem<OUT>::st(y, q, o[q]);
-      }
+      store4<DUAL, OUT>(p, g, r, n0 + c, p.sx[p.row_token ? p.row_token[r] : r], s1, DUAL ? total(row, OC + c) : s1);
     }
     __syncthreads();  // the next tile's copies overwrite the partial sums
   }
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Between those and the 256 x 256 tiles: MT rows x 128 channels (DUAL: 64 of
+// the gate, 64 of the up), whose operands the four waves share in LDS, in
+// chunks of 128 codes of k through two stages.  MT = 64: a wave has 32
+// channels and all rows; MT = 128: 64 channels and half of the rows.  Copies,
+// swizzle and fragments as above.  Two or more workgroups share a CU, so one's
+// waits, barriers and epilogue pass under the others' copies.  Blocks of 16
+// rows that the m-tile does not have are left out.  With half the copies of the
+// rows per weight of the kernel above, it is ahead where these count: gate/up
+// as there with 43 rows each 408 against 457 us, with 21 rows 388 against 372
+// (three stages and two workgroups: 433).
+//   The channel tile fixes the XCD (workgroup id mod 8), so the m-tiles of a
+// group, which follow one another, find its weights in the XCD's L2.
+template <int MT, int WGS, bool DUAL, typename OUT>
+__global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
+  using namespace dma;
+  constexpr int NT = 128, OC = DUAL ? 64 : 128;
+  constexpr int WM = MT / 64, WN = 4 / WM;       // waves over rows and channels
+  constexpr int MB = 4, NB = NT / WN / 16;       // a wave's blocks of 16 rows and 16 channels
+  constexpr int STAGE = (MT + NT) * 128;
+  constexpr int PER = (MT + NT) / 32;            // copies per wave and chunk
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
 
-template <int MB, int NB, int NST, bool DUAL, typename OUT>
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int ntiles = (p.N + OC - 1) / OC, ntiles8 = (ntiles + 7) & ~7;
+  for (int64_t id = blockIdx.x; id < p.tiles; id += gridDim.x) {
+    const int ntile = (int)(id % ntiles8);
+    if (ntile >= ntiles) continue;
+    int g, m0, mlim;
+    if (!find_tile<MT>(p, (int)(id / ntiles8), lane, g, m0, mlim)) break;
+    const int n0 = ntile * OC, nlim = min(OC, p.N - n0);
+    const i32x4 rw = make_rsrc(p.w + ((int64_t)g * p.N + n0) * p.ldw, (uint64_t)nlim * p.ldw);
+    const i32x4 rw2 = DUAL ? make_rsrc(p.w2 + ((int64_t)g * p.N + n0) * p.ldw, (uint64_t)nlim * p.ldw) : rw;
+    const i32x4 rx = p.row_token ? make_rsrc(p.x, (uint64_t)p.x_rows * p.ldx)
+                                 : make_rsrc(p.x + (int64_t)m0 * p.ldx, (uint64_t)mlim * p.ldx);
+    // A wave copies four times 8 of the weight rows, then its share of the
+    // token rows.  With DUAL a wave's channel blocks are gate, up, gate, up ..:
+    // LDS weight row r is gate or up by bit 4, channel 16 (r / 32) + r % 16.
+    uint32_t v[PER];
+    auto row8 = [&](int j) { return j < NT / 32 ? 8 * (wave * (NT / 32) + j) : NT + 8 * (wave * (MT / 32) + j - NT / 32); };
+    auto piece = [&](int j) { return ((lane & 7) ^ swz_k<64>(row8(j) + (lane >> 3))) << 4; };
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int row = row8(j) + (lane >> 3);
+      if (j < NT / 32) {
+        const int src = DUAL ? (row >> 5) * 16 + (row & 15) : row;
+        v[j] = src < nlim ? (uint32_t)(src * p.ldw) + piece(j) : 0x80000000u;
+      } else {
+        const int m = row - NT;
+        uint32_t src = m;
+        if (p.row_token && m < mlim) src = p.row_token[m0 + m];
+        v[j] = m < mlim ? (uint32_t)(src * p.ldx) + piece(j) : 0x80000000u;
+      }
+    }
+    const int chunks = (p.K + 127) / 128;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+    auto copy = [&](int i) {
+      const int k0 = i * 128;
+      const uint32_t st = lds + (uint32_t)(i & 1) * STAGE;
+      const bool whole = k0 + 128 <= p.K;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        uint32_t o = v[j];
+        if (!whole && k0 + piece(j) >= p.K) o = 0x80000000u;
+        const i32x4 r = j >= NT / 32 ? rx : (DUAL && (j & 2) ? rw2 : rw);
+        dma16(r, o, (uint32_t)k0, __builtin_amdgcn_readfirstlane(st + row8(j) * 128));
+      }
+    };
+
+    const int blocks = (min(64, mlim - wm * 64) + 15) / 16;  // the wave's row blocks that exist (may be <= 0)
+    i32x4_t acc[NB][MB];
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+#pragma unroll
+      for (int b = 0; b < MB; ++b) acc[a][b] = i32x4_t{0, 0, 0, 0};
+    copy(0);
+    for (int i = 0; i < chunks; ++i) {
+      wait_vm<0>();
+      lds_barrier();  // chunk i has landed for every wave, and every wave has read chunk i - 1
+      if (i + 1 < chunks) copy(i + 1);
+      const uint8_t* st = smem + (i & 1) * STAGE;
+      const bool tail = i * 128 + 128 > p.K && p.K % 16;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        i32x4_t fw[NB];
+#pragma unroll
+        for (int a = 0; a < NB; ++a) {
+          const int r = (wn * NB + a) * 16 + (lane & 15);
+          fw[a] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+          if (tail) fw[a] = mask_k(fw[a], p.K - (i * 128 + ks * 64 + (lane >> 4) * 16));
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          if (b >= blocks) break;
+          const int r = NT + wm * 64 + b * 16 + (lane & 15);
+          const i32x4_t fx =
+              *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+#pragma unroll
+          for (int a = 0; a < NB; ++a)
+            acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[a], fx, acc[a][b], 0, 0, 0);
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int row = wm * 64 + b * 16 + (lane & 15);
+      if (row >= mlim) continue;
+      const int64_t r = (int64_t)m0 + row;
+      const float sx = p.sx[p.row_token ? p.row_token[r] : r];
+#pragma unroll
+      for (int a = 0; a < NB; a += DUAL ? 2 : 1) {
+        const int c = (wn * NB + a) * (DUAL ? 8 : 16) + (lane >> 4) * 4;
+        if (c < nlim) store4<DUAL, OUT>(p, g, r, n0 + c, sx, acc[a][b], acc[DUAL ? a + 1 : a][b]);
+      }
+    }
+    lds_barrier();  // every wave has read the last chunk before the next tile's copies
+  }
+}
+
+template <int MT, int WGS, bool DUAL, typename OUT>
+hipError_t run_mid(I8Params p, int64_t rows, hipStream_t s) {
+  const int64_t slots = p.offsets ? rows / MT + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MT);
+  p.tiles = slots * (cdiv(cdiv(p.N, DUAL ? 64 : 128), 8) * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);
+  i8_mid_rows_kernel<MT, WGS, DUAL, OUT><<<grid, 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int MB, int NB, int WGS, bool DUAL, typename OUT>
 hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
   constexpr int OC = NB * 16 / (DUAL ? 2 : 1);
   // m-tiles at most: every group may end in a partial one
   const int64_t slots = p.offsets ? rows / (MB * 16) + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MB * 16);
   p.tiles = slots * cdiv(p.N, OC);
   const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);  // (a launch has fewer than 2^32 threads)
-  i8_few_rows_kernel<MB, NB, NST, DUAL, OUT><<<grid, 256, 0, s>>>(p);
+  i8_few_rows_kernel<MB, NB, WGS, DUAL, OUT><<<grid, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
-// rows: an upper bound of all rows; mean: the expected rows of a group.
+// The kernel and tile by size.  rows: an upper bound of all rows; groups, mean:
+// the groups that have rows and the rows of one of them, as expected from
+// evenly spread routing (a skewed one is computed as well, in more m-tiles).
+//   - Rows of 33 and more: the shared-operand kernel, if it has workgroups
+//     for the chip; its 128-row tiles from 65 rows on.
+//   - A short K (a wave's share of it ends before its copies have got going)
+//     and many tiles: the same with fewer rows too (down, f = 1792, 5 rows each:
+//     189 against 201 us).
+//   - Else the largest tile of the few-rows kernel that still gives 300
+//     workgroups: larger tiles copy the rows fewer times, but below about that
+//     the chip's CUs are not all busy (linear 16 x 6144 x 6144: 32 channels
+//     10.5 us, 64 12.4, 128 16.6; gate/up, 96 experts, 5 rows each: 371, 353,
+//     348).
 template <bool DUAL, typename OUT>
-hipError_t run_i8(const I8Params& p, int64_t rows, int64_t mean, hipStream_t s) {
-  if (mean <= 16) return run_few<1, 4, 2, DUAL, OUT>(p, rows, s);
-  return run_few<4, 4, 2, DUAL, OUT>(p, rows, s);
+hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
+  const int64_t N = DUAL ? 2 * (int64_t)p.N : p.N;
+  auto tiles = [&](int mt, int nt) { return groups * cdiv(mean, mt) * cdiv(N, nt); };
+  if (mean > 64 && tiles(128, 128) >= 512) return run_mid<128, 2, DUAL, OUT>(p, rows, s);
+  if (mean > 32 && tiles(64, 128) >= 512) return run_mid<64, 3, DUAL, OUT>(p, rows, s);
+  if (p.K <= 2048 && tiles(64, 128) >= 1200) return run_mid<64, 3, DUAL, OUT>(p, rows, s);
+  constexpr int64_t FILL = 300;
+  if (mean > 32 && tiles(64, 64) >= FILL) return run_few<4, 4, 2, DUAL, OUT>(p, rows, s);
+  if (mean > 8) {
+    if (mean <= 32 && tiles(32, 128) >= FILL) return run_few<2, 8, 2, DUAL, OUT>(p, rows, s);
+    if (tiles(32, 64) >= FILL) return run_few<2, 4, 3, DUAL, OUT>(p, rows, s);
+    if (tiles(32, 32) >= FILL) return run_few<2, 2, 4, DUAL, OUT>(p, rows, s);
+  } else {
+    if (tiles(16, 128) >= FILL) return run_few<1, 8, 2, DUAL, OUT>(p, rows, s);
+    if (tiles(16, 64) >= FILL) return run_few<1, 4, 3, DUAL, OUT>(p, rows, s);
+  }
+  return run_few<1, 2, 4, DUAL, OUT>(p, rows, s);
+}
+
+// The local experts that have rows, as expected: a token's picks fall on num_local of E experts.
+int64_t hit_experts(const moe_desc& d) {
+  return std::min<int64_t>(d.num_local, std::max<int64_t>(1, (int64_t)d.T * d.k * d.num_local / d.E));
 }
 
 }  // namespace
@@ -467,8 +686,8 @@ hipError_t launch_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64
                                    const int32_t* nrows, int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
   if (rows == 0) return hipSuccess;
   if (dtype == MOE_BF16)
-    return quant_rows(reinterpret_cast<const uint16_t*>(w), rows, cols, ldw, nrows, q, ldq, scale, s);
-  return quant_rows(reinterpret_cast<const float*>(w), rows, cols, ldw, nrows, q, ldq, scale, s);
+    return quant_rows(reinterpret_cast<const uint16_t*>(w), rows, (int)cols, ldw, nrows, q, ldq, scale, s);
+  return quant_rows(reinterpret_cast<const float*>(w), rows, (int)cols, ldw, nrows, q, ldq, scale, s);
 }
 
 hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const int32_t* row_token, const int8_t* xq,
@@ -495,7 +714,7 @@ hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const in
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
   if (d.d % 128 == 0 && d.d >= 512 && mean > 64)
     return launch_gate_up_i8_tiles(d, offsets, row_token, xq, xs, W1q, W1s, W3q, W3s, gu, h, s);
-  return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), mean, s);
+  return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
 
 hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_t* hq, const float* hs,
@@ -516,7 +735,7 @@ hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
   if (d.f % 128 == 0 && d.f >= 512 && mean > 64)
     return launch_down_i8_tiles(d, offsets, hq, hs, W2q, W2s, y_perm, s);
-  return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), mean, s);
+  return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
 
 hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, int64_t ldx, const float* xs,
@@ -541,8 +760,8 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
   if (K % 128 == 0 && K >= 512 && N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 &&
       cdiv(M, 256) * cdiv(N, 256) >= 128)
     return launch_i8_linear_tiles((int)M, (int)N, (int)K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, s);
-  if (dtype == MOE_BF16) return run_i8<false, uint16_t>(p, M, M, s);
-  return run_i8<false, float>(p, M, M, s);
+  if (dtype == MOE_BF16) return run_i8<false, uint16_t>(p, M, 1, M, s);
+  return run_i8<false, float>(p, M, 1, M, s);
 }
 
 }  // namespace moe

@@ -80,6 +80,7 @@ P = 4096  # a 16-byte aligned address that no rejected call reads
     (dict(cols=0), moe.MOE_ERR_INVALID_ARG), (dict(ldw=99), moe.MOE_ERR_INVALID_ARG),
     (dict(ldq=96), moe.MOE_ERR_INVALID_ARG), (dict(ldq=120), moe.MOE_ERR_INVALID_ARG),
     (dict(dtype=2), moe.MOE_ERR_UNSUPPORTED), (dict(dtype=-1), moe.MOE_ERR_UNSUPPORTED),
+    (dict(cols=(1 << 28) + 16, ldw=1 << 29, ldq=1 << 29), moe.MOE_ERR_UNSUPPORTED),
     (dict(rows=0), moe.MOE_OK),
 ])
 def test_quantize_refusals(kw, rc):
