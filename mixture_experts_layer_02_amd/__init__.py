@@ -193,7 +193,8 @@ def _p(t):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    # (the current stream's handle, without making a Stream object: 0.3 us in place of 2.9 on every call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _call(name, desc, *args):
@@ -284,14 +285,14 @@ def expert_gate_up_fp8mm(desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, g
 # attribute reads each.
 def _rows(t, name, dtype, dev):
     """Address and distance in elements of the rows of a 2-D tensor (a row's values lie together)."""
-    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev:
+    ld = t.stride()
+    if t.dtype is not dtype or len(ld) != 2 or t.get_device() != dev:
         raise ValueError(f"{name}: a 2-D {dtype} tensor of the current device ({dev}) is needed, "
-                         f"not {t.dim()}-D {t.dtype} of {t.device}")
+                         f"not {tuple(t.shape)} {t.dtype} of {t.device}")
     n, m = t.shape
-    ld, one = t.stride()
-    if one != 1 and m > 1:
+    if ld[1] != 1 and m > 1:
         raise ValueError(f"{name}: the values of a row must lie together")
-    return t.data_ptr(), ld if n > 1 else (m + 15) // 16 * 16
+    return t.data_ptr(), ld[0] if n > 1 else (m + 15) // 16 * 16
 
 
 def _device(t, name):
@@ -310,8 +311,8 @@ def _flat(t, name, n, dtype, dev):
     return t.data_ptr()
 
 
-def _i8(name, *args):
-    rc = getattr(lib(), name)(*args, _stream())
+def _i8(name, dev, *args):
+    rc = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != MOE_OK:
         raise MoeError(name, rc)
 
@@ -329,7 +330,7 @@ def i8_quantize_rows(w, q, scale, nrows=None):
     if q.shape != w.shape:
         raise ValueError("q must have w's shape")
     if rows:
-        _i8("moe_i8_quantize_rows", wp, MOE_BF16 if bf else MOE_F32, rows, cols, ldw,
+        _i8("moe_i8_quantize_rows", dev, wp, MOE_BF16 if bf else MOE_F32, rows, cols, ldw,
             None if nrows is None else _flat(nrows, "nrows", 1, torch.int32, dev), qp, ldq,
             _flat(scale, "scale", rows, torch.float32, dev))
 
@@ -347,7 +348,7 @@ def i8_linear(xq, xs, wq, ws, y, bias=None):
         raise ValueError("xq [M][K], wq [N][K] and y [M][N] do not fit")
     if M:
         f32 = torch.float32
-        _i8("moe_i8_linear", M, N, K, xp, ldx, _flat(xs, "xs", M, f32, dev), wp, ldw, _flat(ws, "ws", N, f32, dev),
+        _i8("moe_i8_linear", dev, M, N, K, xp, ldx, _flat(xs, "xs", M, f32, dev), wp, ldw, _flat(ws, "ws", N, f32, dev),
             None if bias is None else _flat(bias, "bias", N, f32, dev), yp, ldy, MOE_BF16 if bf else MOE_F32)
 
 
@@ -355,7 +356,7 @@ def expert_gate_up_i8(desc, offsets, row_token, xq, xs, w1q, w1s, w3q, w3s, gu, 
     """gate/up + SwiGLU on INT8 codes with a scale per token and per channel."""
     T, d, f, NL, Rc = desc.T, desc.d, desc.f, desc.num_local, desc.R_cap
     i8, f32, i32, bf, dev = torch.int8, torch.float32, torch.int32, torch.bfloat16, _device(h, "h")
-    _i8("moe_expert_gate_up_i8", ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, i32, dev),
+    _i8("moe_expert_gate_up_i8", dev, ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, i32, dev),
         _flat(row_token, "row_token", Rc, i32, dev), _flat(xq, "xq", T * d, i8, dev), _flat(xs, "xs", T, f32, dev),
         _flat(w1q, "w1q", NL * f * d, i8, dev), _flat(w1s, "w1s", NL * f, f32, dev),
         _flat(w3q, "w3q", NL * f * d, i8, dev), _flat(w3s, "w3s", NL * f, f32, dev),
@@ -366,7 +367,7 @@ def expert_down_i8(desc, offsets, hq, hs, w2q, w2s, y_perm):
     """down on INT8 codes with a scale per row and per channel."""
     d, f, NL, Rc = desc.d, desc.f, desc.num_local, desc.R_cap
     i8, f32, dev = torch.int8, torch.float32, _device(y_perm, "y_perm")
-    _i8("moe_expert_down_i8", ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, torch.int32, dev),
+    _i8("moe_expert_down_i8", dev, ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, torch.int32, dev),
         _flat(hq, "hq", Rc * f, i8, dev), _flat(hs, "hs", Rc, f32, dev), _flat(w2q, "w2q", NL * d * f, i8, dev),
         _flat(w2s, "w2s", NL * d, f32, dev), _flat(y_perm, "y_perm", Rc * d, torch.bfloat16, dev))
 

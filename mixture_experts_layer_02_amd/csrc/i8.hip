@@ -212,18 +212,18 @@ hipError_t quant_rows(const T* w, int64_t rows, int cols, int64_t ldw, const int
   const int64_t nv = cdiv(cols, 64 * N);  // vectors per lane of one wave
   const int64_t cap = (int64_t)num_cus() * 16;
   const bool vec = ldw % N == 0;
-  // A wave per row needs a few rows per CU and a row it can hold.
-  if (vec && nv <= 12 && rows >= (int64_t)num_cus() * 8) {
+  // Short rows, many of them: a wave each (16384 x 1792 bf16: 20 us, 4.5 TB/s;
+  // a workgroup each: 37 us).  Else a workgroup per row (16384 x 6144 bf16: 61
+  // us, 5.0 TB/s; a wave each: 73 us; one row of 6144: 4.3 against 6.2 us).
+  if (vec && nv <= 4 && rows >= 1024) {
     const unsigned grid = (unsigned)std::min(cdiv(rows, 4), cap);
-    if (nv <= 4)
-      i8_quant_rows_kernel<T, 1, 4, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
-    else
-      i8_quant_rows_kernel<T, 1, 12, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
+    i8_quant_rows_kernel<T, 1, 4, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
     return hipGetLastError();
   }
   const unsigned grid = (unsigned)std::min(rows, cap);
   if (!vec) i8_quant_rows_kernel<T, 4, 0, false><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
   else if (nv <= 12) i8_quant_rows_kernel<T, 4, 3, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
+  else if (nv <= 32) i8_quant_rows_kernel<T, 4, 8, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
   else i8_quant_rows_kernel<T, 4, 0, true><<<grid, 256, 0, s>>>(w, rows, cols, ldw, nrows, q, ldq, scale);
   return hipGetLastError();
 }
@@ -514,19 +514,20 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
 // (three stages and two workgroups: 433).
 //   The channel tile fixes the XCD (workgroup id mod 8), so the m-tiles of a
 // group, which follow one another, find its weights in the XCD's L2.
-template <int MT, int WGS, bool DUAL, typename OUT>
-__global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
+template <int MT, int NT, int WM, int WN, int WGS, bool DUAL, typename OUT>
+__global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params p) {
   using namespace dma;
-  constexpr int NT = 128, OC = DUAL ? 64 : 128;
-  constexpr int WM = MT / 64, WN = 4 / WM;       // waves over rows and channels
-  constexpr int MB = 4, NB = NT / WN / 16;       // a wave's blocks of 16 rows and 16 channels
+  constexpr int OC = DUAL ? NT / 2 : NT, W = WM * WN;
+  constexpr int MB = MT / WM / 16, NB = NT / WN / 16;  // a wave's blocks of 16 rows and 16 channels
   constexpr int STAGE = (MT + NT) * 128;
-  constexpr int PER = (MT + NT) / 32;            // copies per wave and chunk
+  constexpr int CW = NT / 8 / W, CX = MT / 8 / W;      // copies per wave and chunk: of weight rows, of token rows
+  constexpr int PER = CW + CX;
+  static_assert(CW % 2 == 0 && NB % 2 == 0 && CX >= 1, "shares of the copies; gate and up blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave / WN, wn = wave % WN;
   const int ntiles = (p.N + OC - 1) / OC, ntiles8 = (ntiles + 7) & ~7;
   for (int64_t id = blockIdx.x; id < p.tiles; id += gridDim.x) {
     const int ntile = (int)(id % ntiles8);
@@ -542,12 +543,12 @@ __global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
     // token rows.  With DUAL a wave's channel blocks are gate, up, gate, up ..:
     // LDS weight row r is gate or up by bit 4, channel 16 (r / 32) + r % 16.
     uint32_t v[PER];
-    auto row8 = [&](int j) { return j < NT / 32 ? 8 * (wave * (NT / 32) + j) : NT + 8 * (wave * (MT / 32) + j - NT / 32); };
+    auto row8 = [&](int j) { return j < CW ? 8 * (wave * CW + j) : NT + 8 * (wave * CX + j - CW); };
     auto piece = [&](int j) { return ((lane & 7) ^ swz_k<64>(row8(j) + (lane >> 3))) << 4; };
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int row = row8(j) + (lane >> 3);
-      if (j < NT / 32) {
+      if (j < CW) {
         const int src = DUAL ? (row >> 5) * 16 + (row & 15) : row;
         v[j] = src < nlim ? (uint32_t)(src * p.ldw) + piece(j) : 0x80000000u;
       } else {
@@ -567,12 +568,14 @@ __global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
       for (int j = 0; j < PER; ++j) {
         uint32_t o = v[j];
         if (!whole && k0 + piece(j) >= p.K) o = 0x80000000u;
-        const i32x4 r = j >= NT / 32 ? rx : (DUAL && (j & 2) ? rw2 : rw);
+        // (with DUAL bit 4 of an LDS weight row is a bit of j, or of the wave when it copies two times 8 rows)
+        const i32x4 r = j >= CW ? rx : (DUAL && (CW == 2 ? wave & 1 : j & 2) ? rw2 : rw);
         dma16(r, o, (uint32_t)k0, __builtin_amdgcn_readfirstlane(st + row8(j) * 128));
       }
     };
 
-    const int blocks = (min(64, mlim - wm * 64) + 15) / 16;  // the wave's row blocks that exist (may be <= 0)
+    // The tile's row blocks go to the wave rows in turn; a wave's that exist:
+    const int blocks = ((mlim + 15) / 16 - wm + WM - 1) / WM;
     i32x4_t acc[NB][MB];
 #pragma unroll
     for (int a = 0; a < NB; ++a)
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
           if (b >= blocks) break;
-          const int r = NT + wm * 64 + b * 16 + (lane & 15);
+          const int r = NT + (b * WM + wm) * 16 + (lane & 15);
           const i32x4_t fx =
               *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
 #pragma unroll
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
     }
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
-      const int row = wm * 64 + b * 16 + (lane & 15);
+      const int row = (b * WM + wm) * 16 + (lane & 15);
       if (row >= mlim) continue;
       const int64_t r = (int64_t)m0 + row;
       const float sx = p.sx[p.row_token ? p.row_token[r] : r];
@@ -622,12 +625,12 @@ __global__ void __launch_bounds__(256, WGS) i8_mid_rows_kernel(I8Params p) {
   }
 }
 
-template <int MT, int WGS, bool DUAL, typename OUT>
+template <int MT, int NT, int WM, int WN, int WGS, bool DUAL, typename OUT>
 hipError_t run_mid(I8Params p, int64_t rows, hipStream_t s) {
   const int64_t slots = p.offsets ? rows / MT + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MT);
-  p.tiles = slots * (cdiv(cdiv(p.N, DUAL ? 64 : 128), 8) * 8);
+  p.tiles = slots * (cdiv(cdiv(p.N, DUAL ? NT / 2 : NT), 8) * 8);
   const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);
-  i8_mid_rows_kernel<MT, WGS, DUAL, OUT><<<grid, 256, 0, s>>>(p);
+  i8_mid_rows_kernel<MT, NT, WM, WN, WGS, DUAL, OUT><<<grid, 64 * WM * WN, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -646,7 +649,8 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
 // the groups that have rows and the rows of one of them, as expected from
 // evenly spread routing (a skewed one is computed as well, in more m-tiles).
 //   - Rows of 33 and more: the shared-operand kernel, if it has workgroups
-//     for the chip; its 128-row tiles from 65 rows on.
+//     for the chip; its 128-row tiles from 49 rows on (gate/up, 96 experts, 43
+//     rows each: 64-row tiles 412 us, 128-row 448; 63 rows: 520 and 464).
 //   - A short K (a wave's share of it ends before its copies have got going)
 //     and many tiles: the same with fewer rows too (down, f = 1792, 5 rows each:
 //     189 against 201 us).
@@ -659,9 +663,9 @@ template <bool DUAL, typename OUT>
 hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
   const int64_t N = DUAL ? 2 * (int64_t)p.N : p.N;
   auto tiles = [&](int mt, int nt) { return groups * cdiv(mean, mt) * cdiv(N, nt); };
-  if (mean > 64 && tiles(128, 128) >= 512) return run_mid<128, 2, DUAL, OUT>(p, rows, s);
-  if (mean > 32 && tiles(64, 128) >= 512) return run_mid<64, 3, DUAL, OUT>(p, rows, s);
-  if (p.K <= 2048 && tiles(64, 128) >= 1200) return run_mid<64, 3, DUAL, OUT>(p, rows, s);
+  if (mean > 48 && tiles(128, 128) >= 512) return run_mid<128, 128, 2, 2, 2, DUAL, OUT>(p, rows, s);
+  if (mean > 32 && tiles(64, 128) >= 512) return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, s);
+  if (p.K <= 2048 && tiles(64, 128) >= 1200) return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, s);
   constexpr int64_t FILL = 300;
   if (mean > 32 && tiles(64, 64) >= FILL) return run_few<4, 4, 2, DUAL, OUT>(p, rows, s);
   if (mean > 8) {
@@ -673,6 +677,15 @@ hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean,
     if (tiles(16, 64) >= FILL) return run_few<1, 4, 3, DUAL, OUT>(p, rows, s);
   }
   return run_few<1, 2, 4, DUAL, OUT>(p, rows, s);
+}
+
+// Whether an expert product goes to the 256 x 256 tiles (whole k-tiles of 128
+// codes, at least four): from 97 rows each on, with a short K from 57 on.
+// Measured, 96 experts: gate/up (K = 6144) 63 rows each 512 us against 464 of
+// the kernel above, 105 rows 531 and 562; down (K = 1792) 43 rows 262 and 259, 63
+// rows 268 and 300.
+bool expert_tiles(int64_t K, int64_t mean) {
+  return K % 128 == 0 && K >= 512 && mean > (K <= 2048 ? 56 : 96);
 }
 
 // The local experts that have rows, as expected: a token's picks fall on num_local of E experts.
@@ -712,7 +725,7 @@ hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const in
   p.ldy = d.f;
   p.gu = reinterpret_cast<uint16_t*>(gu);
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
-  if (d.d % 128 == 0 && d.d >= 512 && mean > 64)
+  if (expert_tiles(d.d, mean))
     return launch_gate_up_i8_tiles(d, offsets, row_token, xq, xs, W1q, W1s, W3q, W3s, gu, h, s);
   return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
@@ -733,7 +746,7 @@ hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_
   p.y = y_perm;
   p.ldy = d.d;
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
-  if (d.f % 128 == 0 && d.f >= 512 && mean > 64)
+  if (expert_tiles(d.f, mean))
     return launch_down_i8_tiles(d, offsets, hq, hs, W2q, W2s, y_perm, s);
   return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
@@ -757,6 +770,9 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
   p.y = y;
   p.ldy = ldy;
   const int64_t esz = dtype == MOE_BF16 ? 2 : 4;
+  // The 256 x 256 tiles: whole k-tiles, output rows as 16-byte vectors, and
+  // tiles for half of the chip at least (4096 x 2048 x 2048, 128 of them: 36 us, as
+  // the kernel of 128 rows; 1000 x 6144 x 1792, 96: 32 us against 27).
   if (K % 128 == 0 && K >= 512 && N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 &&
       cdiv(M, 256) * cdiv(N, 256) >= 128)
     return launch_i8_linear_tiles((int)M, (int)N, (int)K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, s);
