@@ -251,7 +251,8 @@ struct I8Params {
   const int32_t* offsets;
   int ngroups;
   int M, N, K;
-  int64_t tiles;  // m-tile slots times channel tiles
+  int64_t tiles;  // workgroups' worth of work: m-tile slots times channel tiles
+  int by_slot;    // how these go to the XCDs (see tile_of)
   void* y;
   int64_t ldy;
   uint16_t* gu;
@@ -265,6 +266,7 @@ __device__ __forceinline__ bool find_tile(const I8Params& p, int slot, int lane,
   g = 0;
   m0 = slot * MT;
   int m1 = p.M;
+  if (!p.offsets && m0 >= m1) g = -1;
   if (p.offsets) {
     int before = 0;
     g = -1;
@@ -295,18 +297,64 @@ __device__ __forceinline__ bool find_tile(const I8Params& p, int slot, int lane,
   return g >= 0;
 }
 
-// The outputs of one row r and the four channels n .. n + 3 of group g (n a
-// multiple of 4) from their sums: s1 alone, or gate s1 and up s2.
+// The scales (or biases) of channels n .. n + 3 of a row of N at `base`, n a
+// multiple of 4; zeros past N.
+__device__ __forceinline__ f32x4_t load4(const float* base, int n, int N) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (N % 4 == 0) {  // (then rows start at multiples of 16 bytes, and the four are all inside or all outside)
+    if (n < N) v = *reinterpret_cast<const f32x4_t*>(base + n);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < N) v[q] = base[n + q];
+  }
+  return v;
+}
+
+// The scales and bias of a lane's four channels, loaded ahead of their use.
+struct Channels {
+  f32x4_t s1, s2, b;  // of the weight (DUAL: the gate's and the up's); the bias
+  template <bool DUAL>
+  __device__ __forceinline__ void load(const I8Params& p, int g, int n) {
+    s1 = load4(p.sw + (int64_t)g * p.N, n, p.N);
+    if (DUAL) s2 = load4(p.sw2 + (int64_t)g * p.N, n, p.N);
+    else b = p.bias ? load4(p.bias, n, p.N) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+};
+
+// Tile `id` (XCD id mod 8) of a product with ntiles channel tiles: its m-tile
+// slot and channel tile (which may be past the last).  by_slot: an m-tile's
+// channel tiles are all on one XCD, one after the other, so its L2 holds the
+// rows of the few m-tiles in work there.  Else the channel tile fixes the XCD,
+// whose L2 then serves a weight tile to all the m-tiles that share it.
+__device__ __forceinline__ void tile_of(const I8Params& p, int64_t id, int ntiles, int& slot, int& ntile) {
+  const int x = (int)(id & 7);
+  const int64_t j = id >> 3;
+  if (p.by_slot) {
+    slot = (int)(j / ntiles) * 8 + x;
+    ntile = (int)(j % ntiles);
+  } else {
+    const int per = (ntiles + 7) >> 3;
+    slot = (int)(j / per);
+    ntile = (int)(j % per) * 8 + x;
+  }
+}
+int64_t tile_count(const I8Params& p, int64_t slots, int64_t ntiles) {
+  return p.by_slot ? cdiv(slots, 8) * 8 * ntiles : slots * cdiv(ntiles, 8) * 8;
+}
+
+// The outputs of one row r at channels n .. n + 3 (n < N) from their sums: s1
+// alone, or gate s1 and up s2.
 template <bool DUAL, typename OUT>
-__device__ __forceinline__ void store4(const I8Params& p, int g, int64_t r, int n, float sx, i32x4_t s1, i32x4_t s2) {
+__device__ __forceinline__ void store4(const I8Params& p, int64_t r, int n, float sx, const Channels& ch, i32x4_t s1,
+                                       i32x4_t s2) {
   float o[4];
-  const int64_t ch = (int64_t)g * p.N + n;
   if constexpr (DUAL) {
     float gt[4], up[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {  // (N is a multiple of 64)
-      gt[q] = (float)s1[q] * sx * p.sw[ch + q];
-      up[q] = (float)s2[q] * sx * p.sw2[ch + q];
+      gt[q] = (float)s1[q] * sx * ch.s1[q];
+      up[q] = (float)s2[q] * sx * ch.s2[q];
       o[q] = gt[q] * sigmoidf_(gt[q]) * up[q];
     }
     if (p.gu) {
@@ -316,11 +364,7 @@ __device__ __forceinline__ void store4(const I8Params& p, int g, int64_t r, int 
     }
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (n + q >= p.N) break;
-      o[q] = (float)s1[q] * sx * p.sw[ch + q];
-      if (p.bias) o[q] += p.bias[ch + q];
-    }
+    for (int q = 0; q < 4; ++q) o[q] = (float)s1[q] * sx * ch.s1[q] + ch.b[q];
   }
   OUT* y = reinterpret_cast<OUT*>(p.y) + r * p.ldy + n;
   if (p.N % 4 == 0 && p.ldy % 4 == 0) {  // (then the four are inside and their address is aligned)
@@ -333,6 +377,14 @@ __device__ __forceinline__ void store4(const I8Params& p, int g, int64_t r, int 
       if (n + q < p.N) Elem<OUT>::st(y, q, o[q]);
   }
 }
+
+// LDS rows are 128 bytes; the 16-byte piece c of row r sits at c ^ swz16(r).  A
+// ds_read_b128 goes by groups of 16 lanes (0-3, 12-15, 20-23, 24-27, the rest
+// of the first 32, and likewise the second), and a fragment's lane l reads
+// piece c + l / 16 of row l % 16: with this swizzle a group's 16 pieces are
+// spread over all 64 banks (none of the reads conflicts; with gemm_dma.h's,
+// made for 32 rows of one piece, half of the read cycles did).
+__device__ __forceinline__ int swz16(int r) { return r & 6; }
 
 // Zeroes the codes at k >= K of a fragment whose lane holds 16 codes from k on.
 __device__ __forceinline__ i32x4_t mask_k(i32x4_t f, int left) {
@@ -362,7 +414,7 @@ __device__ __forceinline__ i32x4_t mask_k(i32x4_t f, int left) {
 //   as columns; lane l holds 16 codes of row l % 16 at k = 16 (l / 16), and
 //   the result's rows 4 (l / 16) .. + 3 of column l % 16, so a lane's four
 //   sums are consecutive channels of one token.
-//   LDS: rows of 128 bytes, 16-byte piece c of row r at c ^ swz_k(r).
+//   LDS: rows of 128 bytes, 16-byte piece c of row r at c ^ swz16(r).
 template <int MB, int NB, int WGS, bool DUAL, typename OUT>
 __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
   using namespace dma;
@@ -379,8 +431,9 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ntiles = (p.N + OC - 1) / OC;
   for (int64_t id = blockIdx.x; id < p.tiles; id += gridDim.x) {
-    const int ntile = (int)(id % ntiles);
-    const int slot = (int)(id / ntiles);
+    int slot, ntile;
+    tile_of(p, id, ntiles, slot, ntile);
+    if (ntile >= ntiles) continue;
 
     int g, m0, mlim;
     if (!find_tile<MT>(p, slot, lane, g, m0, mlim)) break;  // (every later slot is past the last m-tile too)
@@ -394,7 +447,7 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
     const i32x4 rx = p.row_token ? make_rsrc(p.x, (uint64_t)p.x_rows * p.ldx)
                                  : make_rsrc(p.x + (int64_t)m0 * p.ldx, (uint64_t)mlim * p.ldx);
     uint32_t vw[NT / 8], vx[MT / 8];
-    auto piece = [&](int row) { return (lane & 7) ^ swz_k<64>(row); };
+    auto piece = [&](int row) { return (lane & 7) ^ swz16(row); };
 #pragma unroll
     for (int j = 0; j < NT / 8; ++j) {
       const int row = 8 * j + (lane >> 3), src = DUAL && row >= OC ? row - OC : row;
@@ -413,19 +466,23 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
     const uint32_t st_lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * STAGE;
     const uint8_t* st = smem + wave * STAGE;
     auto k_of = [&](int i) { return (wave + 4 * i) * 128; };
-    auto copy = [&](int i) {
-      const int k0 = k_of(i);
-      const bool whole = k0 + 128 <= p.K;
+    // The wave's chunk i.  TAIL: it is K's last and not whole: a piece past K
+    // lies in the next row, and none of it is wanted.
+    auto copy_as = [&](int k0, auto tail_c) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const bool tok = j >= NT / 8;
         const int jj = tok ? j - NT / 8 : j;
         uint32_t v = tok ? vx[tok ? jj : 0] : vw[tok ? 0 : jj];
-        // (a piece past K lies in the next row: none of it is wanted)
-        if (!whole && k0 + piece(8 * jj + (lane >> 3)) * 16 >= p.K) v = 0x80000000u;
+        if (decltype(tail_c)::value && k0 + piece(8 * jj + (lane >> 3)) * 16 >= p.K) v = 0x80000000u;
         const i32x4 r = tok ? rx : (DUAL && j >= NT / 16 ? rw2 : rw);
         dma16(r, v, (uint32_t)k0, __builtin_amdgcn_readfirstlane(st_lds + j * 1024));
       }
+    };
+    auto copy = [&](int i) {
+      const int k0 = k_of(i);
+      if (k0 + 128 <= p.K) copy_as(k0, std::false_type());
+      else copy_as(k0, std::true_type());
     };
 
     i32x4_t acc[NB][MB];
@@ -434,8 +491,21 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
 #pragma unroll
       for (int b = 0; b < MB; ++b) acc[a][b] = i32x4_t{0, 0, 0, 0};
 
-    if (mine > 0) copy(0);
-    for (int i = 0; i < mine; ++i) {
+    // The epilogue's scales, asked for now: thread tid has the channels c_out ..
+    // + 3 of rows tid / VPR, + RPI, ...
+    constexpr int VPR = OC / 4, RPI = 256 / VPR, IT = (MT + RPI - 1) / RPI;
+    const int c_out = (tid % VPR) * 4;
+    Channels ch;
+    ch.template load<DUAL>(p, g, n0 + c_out);
+    float sx[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int row = tid / VPR + i * RPI;
+      sx[i] = row < mlim ? p.sx[p.row_token ? p.row_token[m0 + row] : m0 + row] : 0.f;
+    }
+
+    // A chunk to registers, the next one's copies, its products.
+    auto step = [&](int i, auto tail_c) {
       wait_vm<0>();
       asm volatile("" ::: "memory");
       i32x4_t fw[2][NB], fx[2][MB];
@@ -445,26 +515,25 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
         for (int b = 0; b < MB; ++b) {
           const int r = b * 16 + (lane & 15);
           fx[ks][b] = *reinterpret_cast<const i32x4_t*>(st + (NT + r) * 128 +
-                                                         (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+                                                         (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
         }
 #pragma unroll
         for (int a = 0; a < NB; ++a) {
           const int r = a * 16 + (lane & 15);
-          fw[ks][a] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+          fw[ks][a] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
         }
       }
       // The chunk is in registers before the next one is copied over it.
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       asm volatile("" ::: "memory");
       if (i + 1 < mine) copy(i + 1);
-      const int k0 = k_of(i);
-      if (k0 + 128 > p.K && p.K % 16) {
+      if constexpr (decltype(tail_c)::value) {
         // the codes past K in the row's last piece are not the caller's to give:
         // zeroed in one operand, the other's do not matter
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int b = 0; b < MB; ++b) fx[ks][b] = mask_k(fx[ks][b], p.K - (k0 + ks * 64 + (lane >> 4) * 16));
+          for (int b = 0; b < MB; ++b) fx[ks][b] = mask_k(fx[ks][b], p.K - (k_of(i) + ks * 64 + (lane >> 4) * 16));
       }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
@@ -473,7 +542,12 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
 #pragma unroll
           for (int b = 0; b < MB; ++b)
             acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[ks][a], fx[ks][b], acc[a][b], 0, 0, 0);
-    }
+    };
+    const bool tail = p.K % 16 && mine > 0 && k_of(mine - 1) + 128 > p.K;  // the wave's last chunk needs the mask
+    const int plain = tail ? mine - 1 : mine;
+    if (mine > 0) copy(0);
+    for (int i = 0; i < plain; ++i) step(i, std::false_type());
+    if (tail) step(plain, std::true_type());
 
     // Partial sums [wave][token][channel] over the ring, once every wave is done with it.
     __syncthreads();
@@ -490,30 +564,29 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
       for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const i32x4_t*>(red + (w * MT + row) * RP + c);
       return v;
     };
-    constexpr int VPR = OC / 4;  // vectors of four channels per row
-    for (int e = tid; e < mlim * VPR; e += 256) {
-      const int row = e / VPR, c = (e % VPR) * 4;
-      if (c >= nlim) continue;
-      const int64_t r = (int64_t)m0 + row;
-      const i32x4_t s1 = total(row, c);
-      store4<DUAL, OUT>(p, g, r, n0 + c, p.sx[p.row_token ? p.row_token[r] : r], s1, DUAL ? total(row, OC + c) : s1);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int row = tid / VPR + i * RPI;
+      if (row < mlim && c_out < nlim) {
+        const i32x4_t s1 = total(row, c_out);
+        store4<DUAL, OUT>(p, (int64_t)m0 + row, n0 + c_out, sx[i], ch, s1, DUAL ? total(row, OC + c_out) : s1);
+      }
     }
     __syncthreads();  // the next tile's copies overwrite the partial sums
   }
 }
 
-// Between those and the 256 x 256 tiles: MT rows x 128 channels (DUAL: 64 of
-// the gate, 64 of the up), whose operands the four waves share in LDS, in
-// chunks of 128 codes of k through two stages.  MT = 64: a wave has 32
-// channels and all rows; MT = 128: 64 channels and half of the rows.  Copies,
-// swizzle and fragments as above.  Two or more workgroups share a CU, so one's
-// waits, barriers and epilogue pass under the others' copies.  Blocks of 16
-// rows that the m-tile does not have are left out.  With half the copies of the
-// rows per weight of the kernel above, it is ahead where these count: gate/up
-// as there with 43 rows each 408 against 457 us, with 21 rows 388 against 372
-// (three stages and two workgroups: 433).
-//   The channel tile fixes the XCD (workgroup id mod 8), so the m-tiles of a
-// group, which follow one another, find its weights in the XCD's L2.
+// Between those and the 256 x 256 tiles: MT rows x NT channels (DUAL: half of
+// them gate, half up), whose operands WM x WN waves share in LDS, in chunks of
+// 128 codes of k through two stages; a wave has MT / WM rows and NT / WN
+// channels.  Copies, swizzle and fragments as above.  Two or more workgroups
+// share a CU, so one's waits, barriers and epilogue pass under the others'
+// copies.  Blocks of 16 rows that the m-tile does not have are left out: the
+// loop is built for each number of them (in steps of a quarter), so that it has
+// no branch and reads all its fragments before it multiplies (with branches
+// and one fragment at a time linear 1000 x 6144 x 1792 took 27 us, now 19).
+// It copies the rows half as often per weight as the kernel above, and is ahead
+// where these count: gate/up of 96 experts, 43 rows each, 387 against 433 us.
 template <int MT, int NT, int WM, int WN, int WGS, bool DUAL, typename OUT>
 __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params p) {
   using namespace dma;
@@ -522,18 +595,19 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
   constexpr int STAGE = (MT + NT) * 128;
   constexpr int CW = NT / 8 / W, CX = MT / 8 / W;      // copies per wave and chunk: of weight rows, of token rows
   constexpr int PER = CW + CX;
+  constexpr int KB = NB * MB > 16 ? 1 : 2;             // k-steps whose fragments are read at once
   static_assert(CW % 2 == 0 && NB % 2 == 0 && CX >= 1, "shares of the copies; gate and up blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int ntiles = (p.N + OC - 1) / OC, ntiles8 = (ntiles + 7) & ~7;
+  const int ntiles = (p.N + OC - 1) / OC;
   for (int64_t id = blockIdx.x; id < p.tiles; id += gridDim.x) {
-    const int ntile = (int)(id % ntiles8);
+    int slot, ntile, g, m0, mlim;
+    tile_of(p, id, ntiles, slot, ntile);
     if (ntile >= ntiles) continue;
-    int g, m0, mlim;
-    if (!find_tile<MT>(p, (int)(id / ntiles8), lane, g, m0, mlim)) break;
+    if (!find_tile<MT>(p, slot, lane, g, m0, mlim)) break;
     const int n0 = ntile * OC, nlim = min(OC, p.N - n0);
     const i32x4 rw = make_rsrc(p.w + ((int64_t)g * p.N + n0) * p.ldw, (uint64_t)nlim * p.ldw);
     const i32x4 rw2 = DUAL ? make_rsrc(p.w2 + ((int64_t)g * p.N + n0) * p.ldw, (uint64_t)nlim * p.ldw) : rw;
@@ -544,7 +618,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
     // LDS weight row r is gate or up by bit 4, channel 16 (r / 32) + r % 16.
     uint32_t v[PER];
     auto row8 = [&](int j) { return j < CW ? 8 * (wave * CW + j) : NT + 8 * (wave * CX + j - CW); };
-    auto piece = [&](int j) { return ((lane & 7) ^ swz_k<64>(row8(j) + (lane >> 3))) << 4; };
+    auto piece = [&](int j) { return ((lane & 7) ^ swz16(row8(j) + (lane >> 3))) << 4; };
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int row = row8(j) + (lane >> 3);
@@ -560,18 +634,20 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
     }
     const int chunks = (p.K + 127) / 128;
     const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
-    auto copy = [&](int i) {
-      const int k0 = i * 128;
+    auto copy_as = [&](int i, auto tail_c) {  // (TAIL as above)
       const uint32_t st = lds + (uint32_t)(i & 1) * STAGE;
-      const bool whole = k0 + 128 <= p.K;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         uint32_t o = v[j];
-        if (!whole && k0 + piece(j) >= p.K) o = 0x80000000u;
+        if (decltype(tail_c)::value && i * 128 + piece(j) >= p.K) o = 0x80000000u;
         // (with DUAL bit 4 of an LDS weight row is a bit of j, or of the wave when it copies two times 8 rows)
         const i32x4 r = j >= CW ? rx : (DUAL && (CW == 2 ? wave & 1 : j & 2) ? rw2 : rw);
-        dma16(r, o, (uint32_t)k0, __builtin_amdgcn_readfirstlane(st + row8(j) * 128));
+        dma16(r, o, (uint32_t)(i * 128), __builtin_amdgcn_readfirstlane(st + row8(j) * 128));
       }
+    };
+    auto copy = [&](int i) {
+      if (i * 128 + 128 <= p.K) copy_as(i, std::false_type());
+      else copy_as(i, std::true_type());
     };
 
     // The tile's row blocks go to the wave rows in turn; a wave's that exist:
@@ -581,54 +657,91 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
     for (int a = 0; a < NB; ++a)
 #pragma unroll
       for (int b = 0; b < MB; ++b) acc[a][b] = i32x4_t{0, 0, 0, 0};
-    copy(0);
-    for (int i = 0; i < chunks; ++i) {
+
+    // The epilogue's scales, asked for now.
+    constexpr int AS = DUAL ? 2 : 1;  // weight blocks of an output block
+    auto c_out = [&](int a) { return (wn * NB + a) * (DUAL ? 8 : 16) + (lane >> 4) * 4; };
+    Channels ch[NB / AS];
+    float sx[MB];
+#pragma unroll
+    for (int a = 0; a < NB; a += AS) ch[a / AS].template load<DUAL>(p, g, n0 + c_out(a));
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int row = (b * WM + wm) * 16 + (lane & 15);
+      sx[b] = row < mlim ? p.sx[p.row_token ? p.row_token[m0 + row] : m0 + row] : 0.f;
+    }
+
+    // Chunk i: the next one's copies, its fragments, its products with the
+    // first MBA row blocks.
+    auto step = [&](int i, auto mba_c, auto tail_c) {
+      constexpr int MBA = decltype(mba_c)::value;
       wait_vm<0>();
       lds_barrier();  // chunk i has landed for every wave, and every wave has read chunk i - 1
       if (i + 1 < chunks) copy(i + 1);
       const uint8_t* st = smem + (i & 1) * STAGE;
-      const bool tail = i * 128 + 128 > p.K && p.K % 16;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        i32x4_t fw[NB];
+      for (int k = 0; k < 2; k += KB) {
+        i32x4_t fw[KB][NB], fx[KB][MBA > 0 ? MBA : 1];
 #pragma unroll
-        for (int a = 0; a < NB; ++a) {
-          const int r = (wn * NB + a) * 16 + (lane & 15);
-          fw[a] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
-          if (tail) fw[a] = mask_k(fw[a], p.K - (i * 128 + ks * 64 + (lane >> 4) * 16));
+        for (int kk = 0; kk < KB; ++kk) {
+          const int ks = k + kk;
+#pragma unroll
+          for (int a = 0; a < (MBA > 0 ? NB : 0); ++a) {
+            const int r = (wn * NB + a) * 16 + (lane & 15);
+            fw[kk][a] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
+            if constexpr (decltype(tail_c)::value)
+              fw[kk][a] = mask_k(fw[kk][a], p.K - (i * 128 + ks * 64 + (lane >> 4) * 16));
+          }
+#pragma unroll
+          for (int b = 0; b < MBA; ++b) {
+            const int r = NT + (b * WM + wm) * 16 + (lane & 15);
+            fx[kk][b] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
+          }
         }
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-          if (b >= blocks) break;
-          const int r = NT + (b * WM + wm) * 16 + (lane & 15);
-          const i32x4_t fx =
-              *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz_k<64>(r)) << 4));
+        for (int kk = 0; kk < KB; ++kk)
 #pragma unroll
-          for (int a = 0; a < NB; ++a)
-            acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[a], fx, acc[a][b], 0, 0, 0);
-        }
+          for (int b = 0; b < MBA; ++b)
+#pragma unroll
+            for (int a = 0; a < NB; ++a)
+              acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[kk][a], fx[kk][b], acc[a][b], 0, 0, 0);
       }
+    };
+    const bool tail = p.K % 16 != 0;  // the last chunk needs the mask
+    const int plain = tail ? chunks - 1 : chunks;
+    auto loop = [&](auto mba_c) {
+      for (int i = 0; i < plain; ++i) step(i, mba_c, std::false_type());
+      if (tail) step(plain, mba_c, std::true_type());
+    };
+    copy(0);
+    constexpr int Q = (MB + 3) / 4;  // a loop for each number of row blocks, in steps of a quarter of all
+    switch ((blocks + Q - 1) / Q) {
+      case 0: loop(std::integral_constant<int, 0>()); break;
+      case 1: loop(std::integral_constant<int, Q>()); break;
+      case 2: loop(std::integral_constant<int, MB < 2 * Q ? MB : 2 * Q>()); break;
+      case 3: loop(std::integral_constant<int, MB < 3 * Q ? MB : 3 * Q>()); break;
+      default: loop(std::integral_constant<int, MB>()); break;
     }
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       const int row = (b * WM + wm) * 16 + (lane & 15);
       if (row >= mlim) continue;
-      const int64_t r = (int64_t)m0 + row;
-      const float sx = p.sx[p.row_token ? p.row_token[r] : r];
 #pragma unroll
-      for (int a = 0; a < NB; a += DUAL ? 2 : 1) {
-        const int c = (wn * NB + a) * (DUAL ? 8 : 16) + (lane >> 4) * 4;
-        if (c < nlim) store4<DUAL, OUT>(p, g, r, n0 + c, sx, acc[a][b], acc[DUAL ? a + 1 : a][b]);
-      }
+      for (int a = 0; a < NB; a += AS)
+        if (c_out(a) < nlim)
+          store4<DUAL, OUT>(p, (int64_t)m0 + row, n0 + c_out(a), sx[b], ch[a / AS], acc[a][b], acc[a + AS - 1][b]);
     }
     lds_barrier();  // every wave has read the last chunk before the next tile's copies
   }
 }
 
 template <int MT, int NT, int WM, int WN, int WGS, bool DUAL, typename OUT>
-hipError_t run_mid(I8Params p, int64_t rows, hipStream_t s) {
+hipError_t run_mid(I8Params p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
+  // One m-tile per group: nothing shares its weights, so its rows are kept
+  // together (gate/up, 105 rows each: 476 us against 515 by channel tiles).
+  p.by_slot = p.offsets && groups >= 32 && mean <= MT - MT / 16;
   const int64_t slots = p.offsets ? rows / MT + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MT);
-  p.tiles = slots * (cdiv(cdiv(p.N, DUAL ? NT / 2 : NT), 8) * 8);
+  p.tiles = tile_count(p, slots, cdiv(p.N, DUAL ? NT / 2 : NT));
   const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);
   i8_mid_rows_kernel<MT, NT, WM, WN, WGS, DUAL, OUT><<<grid, 64 * WM * WN, 0, s>>>(p);
   return hipGetLastError();
@@ -639,7 +752,7 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
   constexpr int OC = NB * 16 / (DUAL ? 2 : 1);
   // m-tiles at most: every group may end in a partial one
   const int64_t slots = p.offsets ? rows / (MB * 16) + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MB * 16);
-  p.tiles = slots * cdiv(p.N, OC);
+  p.tiles = tile_count(p, slots, cdiv(p.N, OC));
   const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);  // (a launch has fewer than 2^32 threads)
   i8_few_rows_kernel<MB, NB, WGS, DUAL, OUT><<<grid, 256, 0, s>>>(p);
   return hipGetLastError();
@@ -648,24 +761,28 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
 // The kernel and tile by size.  rows: an upper bound of all rows; groups, mean:
 // the groups that have rows and the rows of one of them, as expected from
 // evenly spread routing (a skewed one is computed as well, in more m-tiles).
-//   - Rows of 33 and more: the shared-operand kernel, if it has workgroups
-//     for the chip; its 128-row tiles from 49 rows on (gate/up, 96 experts, 43
-//     rows each: 64-row tiles 412 us, 128-row 448; 63 rows: 520 and 464).
+// Times of gate/up of 96 experts, K = 6144, N = 2 x 1792, unless said otherwise.
+//   - From 33 rows on the shared-operand kernel, where its tiles fill the chip:
+//     64 rows a tile up to 48 (43 rows each: 387 us; 128 rows a tile 414), then
+//     192 where a group has one such tile and 128 would be two (171 rows: 579
+//     us against 709), else 128 (63 rows: 430 us, 192 rows a tile 443; linear
+//     4096 x 2048 x 2048: 25 us, 192 rows a tile 32, 64 rows 31).
 //   - A short K (a wave's share of it ends before its copies have got going)
-//     and many tiles: the same with fewer rows too (down, f = 1792, 5 rows each:
-//     189 against 201 us).
+//     and many tiles: its 64-row tiles with fewer rows too (down, K = 1792, 3 of 10
+//     experts one row each: 46 us against 51).
 //   - Else the largest tile of the few-rows kernel that still gives 300
 //     workgroups: larger tiles copy the rows fewer times, but below about that
 //     the chip's CUs are not all busy (linear 16 x 6144 x 6144: 32 channels
-//     10.5 us, 64 12.4, 128 16.6; gate/up, 96 experts, 5 rows each: 371, 353,
-//     348).
+//     10.1 us, 64 11.6, 128 15.5; gate/up, 5 rows each: 373, 350, 349).
 template <bool DUAL, typename OUT>
 hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
   const int64_t N = DUAL ? 2 * (int64_t)p.N : p.N;
   auto tiles = [&](int mt, int nt) { return groups * cdiv(mean, mt) * cdiv(N, nt); };
-  if (mean > 48 && tiles(128, 128) >= 512) return run_mid<128, 128, 2, 2, 2, DUAL, OUT>(p, rows, s);
-  if (mean > 32 && tiles(64, 128) >= 512) return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, s);
-  if (p.K <= 2048 && tiles(64, 128) >= 1200) return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, s);
+  if (mean > 104 && mean <= 176 && tiles(192, 128) >= 400)
+    return run_mid<192, 128, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
+  if (mean > 48 && tiles(128, 128) >= 400) return run_mid<128, 128, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
+  if (mean > 32 ? tiles(64, 128) >= 512 : p.K <= 2048 && tiles(64, 128) >= 1200)
+    return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, groups, mean, s);
   constexpr int64_t FILL = 300;
   if (mean > 32 && tiles(64, 64) >= FILL) return run_few<4, 4, 2, DUAL, OUT>(p, rows, s);
   if (mean > 8) {
@@ -679,13 +796,15 @@ hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean,
   return run_few<1, 2, 4, DUAL, OUT>(p, rows, s);
 }
 
-// Whether an expert product goes to the 256 x 256 tiles (whole k-tiles of 128
-// codes, at least four): from 97 rows each on, with a short K from 57 on.
-// Measured, 96 experts: gate/up (K = 6144) 63 rows each 512 us against 464 of
-// the kernel above, 105 rows 531 and 562; down (K = 1792) 43 rows 262 and 259, 63
-// rows 268 and 300.
-bool expert_tiles(int64_t K, int64_t mean) {
-  return K % 128 == 0 && K >= 512 && mean > (K <= 2048 ? 56 : 96);
+// Whether a product goes to the 256 x 256 tiles (whole k-tiles of 128 codes, at
+// least four) instead of the kernels above.  They are ahead where there are
+// many (they run on one workgroup per CU, round by round) and groups have many
+// rows, or K is short: gate/up 171 rows each 595 us against 579, 250 rows 699
+// and 857; down (K = 1792) 43 rows 262 and 237, 63 rows 268 and 272, 105 rows 286
+// and 321; down of 64 experts, K = 1024, 125 rows, 512 tiles: 51 and 43; linear
+// 4096 x 6144 x 6144, 384 tiles: 169 and 158; 16384 rows, 1536: 519 and 638.
+bool use_tiles(int64_t K, int64_t tiles, int64_t mean) {
+  return K % 128 == 0 && K >= 512 && (mean > 176 || (K <= 2048 && mean > 56 && tiles >= 1024));
 }
 
 // The local experts that have rows, as expected: a token's picks fall on num_local of E experts.
@@ -725,7 +844,7 @@ hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const in
   p.ldy = d.f;
   p.gu = reinterpret_cast<uint16_t*>(gu);
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
-  if (expert_tiles(d.d, mean))
+  if (use_tiles(d.d, d.num_local * cdiv(mean, 256) * cdiv(d.f, 128), mean))
     return launch_gate_up_i8_tiles(d, offsets, row_token, xq, xs, W1q, W1s, W3q, W3s, gu, h, s);
   return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
@@ -746,7 +865,7 @@ hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_
   p.y = y_perm;
   p.ldy = d.d;
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
-  if (expert_tiles(d.f, mean))
+  if (use_tiles(d.f, d.num_local * cdiv(mean, 256) * cdiv(d.d, 256), mean))
     return launch_down_i8_tiles(d, offsets, hq, hs, W2q, W2s, y_perm, s);
   return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
@@ -770,11 +889,9 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
   p.y = y;
   p.ldy = ldy;
   const int64_t esz = dtype == MOE_BF16 ? 2 : 4;
-  // The 256 x 256 tiles: whole k-tiles, output rows as 16-byte vectors, and
-  // tiles for half of the chip at least (4096 x 2048 x 2048, 128 of them: 36 us, as
-  // the kernel of 128 rows; 1000 x 6144 x 1792, 96: 32 us against 27).
-  if (K % 128 == 0 && K >= 512 && N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 &&
-      cdiv(M, 256) * cdiv(N, 256) >= 128)
+  // (the tiles store their output rows as 16-byte vectors)
+  const int64_t tiles = cdiv(M, 256) * cdiv(N, 256);
+  if (N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 && tiles >= 768 && use_tiles(K, tiles, M))
     return launch_i8_linear_tiles((int)M, (int)N, (int)K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, s);
   if (dtype == MOE_BF16) return run_i8<false, uint16_t>(p, M, 1, M, s);
   return run_i8<false, float>(p, M, 1, M, s);

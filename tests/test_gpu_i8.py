@@ -125,7 +125,8 @@ def _linear(gpu, M, N, K, dtype, bias, pad=0, seed=0, codes=None):
 @pytest.mark.parametrize("dtype,bias", [("bf16", False), ("f32", True)])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 16, 16), (1, 3, 17), (2, 64, 128), (15, 63, 127), (16, 65, 129), (17, 1003, 1990),
                                    (31, 32, 33), (33, 48, 512), (63, 128, 640), (64, 64, 64), (65, 100, 1000), (1, 3584, 6144),
-                                   (130, 260, 1024), (257, 257, 1024), (300, 520, 2048), (1000, 777, 1537), (513, 1024, 6144)])
+                                   (130, 260, 1024), (257, 257, 1024), (300, 520, 2048), (1000, 777, 1537), (513, 1024, 6144),
+                                   (500, 2500, 100), (1500, 3150, 100), (2600, 2601, 130), (8200, 6144, 512)])
 def test_linear_matches_the_oracle(gpu, M, N, K, dtype, bias):
     _linear(gpu, M, N, K, dtype, bias)
 
@@ -179,6 +180,15 @@ SHAPES = {  # T, d, f, E, k, e0, NL, skew
     "tails of 256": (2300, 1024, 512, 8, 2, 1, 6, 0.0),
     "long": (5000, 768, 640, 16, 4, 0, 16, 0.5),
     "1T sizes": (300, 6144, 1792, 16, 2, 0, 4, 0.0),
+    # enough tiles for the larger tiles of the few-rows kernel and the shared-operand kernel; K in half chunks
+    "6 rows, many tiles": (48, 832, 448, 64, 8, 0, 64, 0.0),
+    "20 rows, many tiles": (160, 832, 448, 64, 8, 0, 64, 0.0),
+    "5 rows, very many tiles": (120, 832, 448, 192, 8, 0, 192, 0.5),
+    "40 rows, many tiles": (480, 832, 448, 96, 8, 0, 96, 0.0),
+    "75 rows, many tiles": (600, 832, 448, 64, 8, 0, 64, 0.0),
+    "125 rows, many tiles": (1000, 832, 448, 64, 8, 0, 64, 0.0),
+    "125 rows, skewed": (1000, 832, 448, 64, 8, 0, 64, 1.0),
+    "500 rows, K no multiple of 128": (2000, 832, 448, 32, 8, 0, 32, 0.3),
 }
 
 
