@@ -400,23 +400,23 @@ __device__ __forceinline__ i32x4_t mask_k(i32x4_t f, int left) {
 // by one workgroup only: the kernel is bound by HBM and has to keep many loads
 // in flight.  A workgroup computes MB*16 rows x NB*16 channels (DUAL: half of
 // them gate, half up) over all of K, cut into chunks of 128 codes that its
-// four waves take in turn; no wave shares an operand with another, so the main
+// W waves take in turn; no wave shares an operand with another, so the main
 // loop has no barrier: each wave copies a chunk into its own part of LDS (LDS
 // DMA, 8 rows x 128 bytes per instruction, all lines whole), waits for it,
 // takes it to registers, starts the next copy over it and multiplies.  Several
-// workgroups share a CU (WGS at least), so a CU's whole LDS is in flight most of
-// the time.  (Measured on gate/up, d = 6144, f = 1792, 96 experts of which 21
-// rows each: 372 us, 5.7 TB/s; a ring of two stages with half the workgroups
-// took 512 us, chunks of 64 codes, half lines, 451 us.)  The four partial sums
-// are whole numbers and are added through LDS at the end, in any order with the
-// same result.
+// workgroups share a CU (at least WPS waves per SIMD), so a CU's whole LDS is in
+// flight most of the time.  (Measured on gate/up, d = 6144, f = 1792, 96 experts
+// of which 21 rows each: 372 us, 5.7 TB/s; a ring of two stages with half the
+// workgroups took 512 us, chunks of 64 codes, half lines, 451 us.)  The W partial
+// sums are whole numbers and are added through LDS at the end, in any order with
+// the same result.
 //   Fragments: v_mfma_i32_16x16x64_i8 with the channels as rows and the tokens
 //   as columns; lane l holds 16 codes of row l % 16 at k = 16 (l / 16), and
 //   the result's rows 4 (l / 16) .. + 3 of column l % 16, so a lane's four
 //   sums are consecutive channels of one token.
 //   LDS: rows of 128 bytes, 16-byte piece c of row r at c ^ swz16(r).
-template <int MB, int NB, int WGS, bool DUAL, typename OUT>
-__global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
+template <int MB, int NB, int W, int WPS, bool DUAL, typename OUT>
+__global__ void __launch_bounds__(64 * W, WPS) i8_few_rows_kernel(I8Params p) {
   using namespace dma;
   static_assert(!DUAL || NB % 2 == 0, "gate and up blocks");
   constexpr int MT = MB * 16, NT = NB * 16;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
   constexpr int STAGE = (MT + NT) * 128;       // bytes: weight rows, then token rows
   constexpr int PER = (MT + NT) / 8;           // copies per chunk
   constexpr int RP = NT + 4;                   // pitch of the partial sums (ints)
-  constexpr int RING = 4 * STAGE, RED = 4 * MT * RP * 4;
+  constexpr int RING = W * STAGE, RED = W * MT * RP * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > RED ? RING : RED];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -462,10 +462,10 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
     }
 
     const int chunks = (p.K + 127) / 128;
-    const int mine = (chunks - wave + 3) / 4;  // chunks wave, wave + 4, ...
+    const int mine = (chunks - wave + W - 1) / W;  // chunks wave, wave + W, ...
     const uint32_t st_lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * STAGE;
     const uint8_t* st = smem + wave * STAGE;
-    auto k_of = [&](int i) { return (wave + 4 * i) * 128; };
+    auto k_of = [&](int i) { return (wave + W * i) * 128; };
     // The wave's chunk i.  TAIL: it is K's last and not whole: a piece past K
     // lies in the next row, and none of it is wanted.
     auto copy_as = [&](int k0, auto tail_c) {
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
 
     // The epilogue's scales, asked for now: thread tid has the channels c_out ..
     // + 3 of rows tid / VPR, + RPI, ...
-    constexpr int VPR = OC / 4, RPI = 256 / VPR, IT = (MT + RPI - 1) / RPI;
+    constexpr int VPR = OC / 4, RPI = 64 * W / VPR, IT = (MT + RPI - 1) / RPI;
     const int c_out = (tid % VPR) * 4;
     Channels ch;
     ch.template load<DUAL>(p, g, n0 + c_out);
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(256, WGS) i8_few_rows_kernel(I8Params p) {
     auto total = [&](int row, int c) {
       i32x4_t v = *reinterpret_cast<const i32x4_t*>(red + row * RP + c);
 #pragma unroll
-      for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const i32x4_t*>(red + (w * MT + row) * RP + c);
+      for (int w = 1; w < W; ++w) v += *reinterpret_cast<const i32x4_t*>(red + (w * MT + row) * RP + c);
       return v;
     };
 #pragma unroll
@@ -747,14 +747,14 @@ hipError_t run_mid(I8Params p, int64_t rows, int64_t groups, int64_t mean, hipSt
   return hipGetLastError();
 }
 
-template <int MB, int NB, int WGS, bool DUAL, typename OUT>
+template <int MB, int NB, int W, int WPS, bool DUAL, typename OUT>
 hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
   constexpr int OC = NB * 16 / (DUAL ? 2 : 1);
   // m-tiles at most: every group may end in a partial one
   const int64_t slots = p.offsets ? rows / (MB * 16) + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MB * 16);
   p.tiles = tile_count(p, slots, cdiv(p.N, OC));
   const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);  // (a launch has fewer than 2^32 threads)
-  i8_few_rows_kernel<MB, NB, WGS, DUAL, OUT><<<grid, 256, 0, s>>>(p);
+  i8_few_rows_kernel<MB, NB, W, WPS, DUAL, OUT><<<grid, 64 * W, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -774,6 +774,10 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
 //     workgroups: larger tiles copy the rows fewer times, but below about that
 //     the chip's CUs are not all busy (linear 16 x 6144 x 6144: 32 channels
 //     10.1 us, 64 11.6, 128 15.5; gate/up, 5 rows each: 373, 350, 349).
+//   - Where no tile gives that many, eight waves on a long K keep twice as many
+//     copies in flight on a CU (linear 1 x 6144 x 6144: 7.9 us, four waves 10.0;
+//     K = 2048: 4.1 both; where the chip is full they lose: gate/up of 12
+//     experts, one row each, 39.0 against 30.6).
 template <bool DUAL, typename OUT>
 hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
   const int64_t N = DUAL ? 2 * (int64_t)p.N : p.N;
@@ -784,16 +788,17 @@ hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean,
   if (mean > 32 ? tiles(64, 128) >= 512 : p.K <= 2048 && tiles(64, 128) >= 1200)
     return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, groups, mean, s);
   constexpr int64_t FILL = 300;
-  if (mean > 32 && tiles(64, 64) >= FILL) return run_few<4, 4, 2, DUAL, OUT>(p, rows, s);
+  if (mean > 32 && tiles(64, 64) >= FILL) return run_few<4, 4, 4, 2, DUAL, OUT>(p, rows, s);
   if (mean > 8) {
-    if (mean <= 32 && tiles(32, 128) >= FILL) return run_few<2, 8, 2, DUAL, OUT>(p, rows, s);
-    if (tiles(32, 64) >= FILL) return run_few<2, 4, 3, DUAL, OUT>(p, rows, s);
-    if (tiles(32, 32) >= FILL) return run_few<2, 2, 4, DUAL, OUT>(p, rows, s);
+    if (mean <= 32 && tiles(32, 128) >= FILL) return run_few<2, 8, 4, 2, DUAL, OUT>(p, rows, s);
+    if (tiles(32, 64) >= FILL) return run_few<2, 4, 4, 3, DUAL, OUT>(p, rows, s);
+    if (tiles(32, 32) >= FILL) return run_few<2, 2, 4, 4, DUAL, OUT>(p, rows, s);
   } else {
-    if (tiles(16, 128) >= FILL) return run_few<1, 8, 2, DUAL, OUT>(p, rows, s);
-    if (tiles(16, 64) >= FILL) return run_few<1, 4, 3, DUAL, OUT>(p, rows, s);
+    if (tiles(16, 128) >= FILL) return run_few<1, 8, 4, 2, DUAL, OUT>(p, rows, s);
+    if (tiles(16, 64) >= FILL) return run_few<1, 4, 4, 3, DUAL, OUT>(p, rows, s);
   }
-  return run_few<1, 2, 4, DUAL, OUT>(p, rows, s);
+  if (p.K >= 4096) return run_few<1, 2, 8, 4, DUAL, OUT>(p, rows, s);
+  return run_few<1, 2, 4, 4, DUAL, OUT>(p, rows, s);
 }
 
 // Whether a product goes to the 256 x 256 tiles (whole k-tiles of 128 codes, at

@@ -143,6 +143,12 @@ def test_linear_sums_of_the_largest_codes_do_not_overflow(gpu, M):
     _linear(gpu, M, 520, K, "f32", False, codes=(np.full((M, K), 127, np.int8), np.full((520, K), -127, np.int8)))
 
 
+@pytest.mark.parametrize("dtype,bias", [("bf16", True), ("f32", False)])
+@pytest.mark.parametrize("M,N,K", [(1, 6144, 4096), (1, 5, 4097), (16, 1003, 4223), (17, 100, 8191), (40, 33, 6000), (130, 31, 131072)])
+def test_linear_of_few_channels_and_a_long_k(gpu, M, N, K, dtype, bias):
+    _linear(gpu, M, N, K, dtype, bias)
+
+
 def test_linear_of_no_rows(gpu):
     w = torch.zeros(8, 16, dtype=torch.int8, device=gpu)
     s = torch.zeros(8, device=gpu)
