@@ -30,15 +30,14 @@ extern "C" {
  *   alone (e.g. offsets + NL: the routed rows of a [R_cap] buffer).  rows may
  *   be 0.  Errors: MOE_ERR_INVALID_ARG for a NULL pointer, w or q not 16-byte
  *   aligned, scale or nrows not 4-byte aligned, or sizes outside these rules;
- *   MOE_ERR_UNSUPPORTED for another dtype
- *   or more than 2^28 cols. */
+ *   MOE_ERR_UNSUPPORTED for another dtype or more than 2^28 cols. */
 int moe_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw,
                          const int32_t* nrows, int8_t* q, int64_t ldq, float* scale, void* stream);
 
 /* A linear layer on INT8 codes (e.g. a dense projection beside the experts):
  *   y[m][n] = xs[m] ws[n] (sum over k of xq[m][k] wq[n][k]) + bias[n]
- *   with the sum in 32-bit integers (exact), the scales and the bias in
- *   float32, rounded once to y's type.
+ *   with the sum in 32-bit integers (exact), then, in float32 and in this order,
+ *   times xs, times ws, plus the bias, and one rounding to y's type.
  *   xq [M][K] codes, rows ldx bytes apart, xs [M]; wq [N][K] codes, rows ldw
  *   bytes apart, ws [N]; bias [N] float32 or NULL; y [M][N] MOE_BF16 or
  *   MOE_F32 as `dtype`, rows ldy >= N elements apart.  Any M >= 0, N >= 1 and

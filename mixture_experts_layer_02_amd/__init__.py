@@ -623,7 +623,9 @@ class Int8Buffers:
 
 def forward_i8(b: Buffers, i8: Int8Buffers, x, wr, experts: Int8Experts, bias=None, routing=None, n_groups=1):
     """forward with the expert products in INT8: the router, the permutation's
-    indices and the combine as there, x and h quantised per row on the way."""
+    indices and the combine as there, x and h quantised per row on the way.
+    It is a serving pass: b.x_perm is not written (make b with gather=True) and
+    the codes have no gradient, so backward is not for its results."""
     D = b.desc
     if routing is None:
         router_logits(D, x, wr, bias, b.logits, b.ws_router)

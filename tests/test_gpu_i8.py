@@ -173,6 +173,37 @@ def test_linear_beyond_32_bit_offsets(gpu):
         del y, wq
 
 
+@pytest.mark.parametrize("M,N,K,ldx,ldw,ldy", [(40, 1100, 300, 1 << 22, 1 << 22, 1 << 26), (1100, 2050, 1536, 1 << 22, 1 << 22, 1 << 21),
+                                               (8200, 6144, 512, 1 << 20, 1 << 20, 1 << 19), (2400001, 1024, 512, 512, 512, 1024)])
+def test_linear_of_rows_far_apart(gpu, M, N, K, ldx, ldw, ldy):
+    """Every operand past 32-bit offsets, through each kind of kernel: sampled rows in whole, every value written."""
+    rng = np.random.default_rng(M)
+    X = torch.empty(M, ldx, dtype=torch.int8, device=gpu)[:, :K]
+    W = torch.empty(N, ldw, dtype=torch.int8, device=gpu)[:, :K]
+    Y = torch.empty(M, ldy, dtype=torch.bfloat16, device=gpu)[:, :N]
+    X.random_(-127, 128)
+    W.random_(-127, 128)
+    Y.fill_(float("nan"))
+    xs, ws = torch.rand(M, device=gpu), torch.rand(N, device=gpu)
+    moe.i8_linear(X, xs, W, ws, Y)
+    assert not torch.isnan(Y).any()
+    m = np.unique(np.concatenate([[0, M - 1], rng.integers(0, M, 30)]))
+    ref = oracle.i8_linear(X[m].cpu().numpy(), xs[m].cpu().numpy(), W.cpu().numpy(), ws.cpu().numpy())
+    _within(to_host(Y[m].contiguous()), ref, 4 * U32 * np.abs(ref), True)
+
+
+def test_quantize_rows_far_apart(gpu):
+    w = torch.empty(70000, 1 << 16, dtype=torch.bfloat16, device=gpu)[:, :300]
+    q = torch.empty(70000, 1 << 16, dtype=torch.int8, device=gpu)[:, :300]
+    w.normal_()
+    s = torch.empty(70000, device=gpu)
+    moe.i8_quantize_rows(w, q, s)
+    for m in (slice(0, 50), slice(32750, 32800), slice(65500, 65560), slice(69950, 70000)):
+        codes, scale = oracle.i8_quantize_rows(w[m].float().cpu().numpy())
+        np.testing.assert_array_equal(q[m].cpu().numpy(), codes)
+        np.testing.assert_array_equal(s[m].cpu().numpy(), scale)
+
+
 # ---- the expert products ----------------------------------------------------
 
 SHAPES = {  # T, d, f, E, k, e0, NL, skew
@@ -356,3 +387,34 @@ def test_python_checks_of_the_expert_calls(gpu):
         moe.expert_down_i8(D, b.offsets, torch.empty(D.R_cap, D.f, device=gpu), a["xs"], a["w1q"], a["w1s"], b.y_perm)
     with pytest.raises(ValueError):
         moe.i8_linear(a["xq"].t(), a["xs"], a["xq"], a["xs"], b.h)
+
+
+@pytest.mark.parametrize("per", [2, 60, 200])
+def test_experts_whose_weights_pass_32_bit_offsets(gpu, per):
+    """96 experts of 25 M weights each, 2.4 GiB a matrix; the last one among those that have rows."""
+    E, d, f = 96, 4096, 6272
+    T = per * E
+    D = moe.make_desc(T, d, f, E, 1, 0, E, "bf16")
+    idx = torch.full((T, 1), E - 1, dtype=torch.int32, device=gpu)
+    idx[: T // 3] = 0
+    b = moe.Buffers(D, gather=True)
+    moe.permute(D, idx, None, b.counts, b.offsets, b.row_token, b.slot_row, None, b.ws_permute)
+    w = [torch.empty(E, r, c, dtype=torch.int8, device=gpu) for r, c in ((f, d), (f, d), (d, f))]
+    s = [torch.rand(E, r, device=gpu) * 1e-3 + 1e-4 for r in (f, f, d)]
+    for v in w:
+        for e in (0, E - 1):
+            v[e].random_(-127, 128)
+    xq = torch.empty(T, d, dtype=torch.int8, device=gpu).random_(-127, 128)
+    hq = torch.empty(T, f, dtype=torch.int8, device=gpu).random_(-127, 128)
+    xs, hs = torch.rand(T, device=gpu) * 1e-3 + 1e-4, torch.rand(T, device=gpu) * 1e-3 + 1e-4
+    moe.expert_gate_up_i8(D, b.offsets, b.row_token, xq, xs, w[0], s[0], w[1], s[1], None, b.h)
+    moe.expert_down_i8(D, b.offsets, hq, hs, w[2], s[2], b.y_perm)
+    tok = b.row_token.cpu().numpy()
+    cut = T // 3
+    for e, rows in ((0, [0, cut - 1]), (E - 1, [cut, (cut + T) // 2, T - 1])):
+        a, z = xq.cpu().numpy()[tok[rows]], xs.cpu().numpy()[tok[rows]]
+        G, U = (oracle.i8_linear(a, z, w[j][e].cpu().numpy(), s[j][e].cpu().numpy()) for j in (0, 1))
+        H = G / (1 + np.exp(-G)) * U
+        _within(to_host(b.h[rows]), H, U32 * (13 + 4 * np.abs(G)) * np.abs(H), True)
+        Y = oracle.i8_linear(hq.cpu().numpy()[rows], hs.cpu().numpy()[rows], w[2][e].cpu().numpy(), s[2][e].cpu().numpy())
+        _within(to_host(b.y_perm[rows]), Y, 3 * U32 * np.abs(Y), True)
