@@ -576,28 +576,31 @@ __global__ void __launch_bounds__(64 * W, WPS) i8_few_rows_kernel(I8Params p) {
   }
 }
 
-// Between those and the 256 x 256 tiles: MT rows x NT channels (DUAL: half of
-// them gate, half up), whose operands WM x WN waves share in LDS, in chunks of
-// 128 codes of k through two stages; a wave has MT / WM rows and NT / WN
-// channels.  Copies, swizzle and fragments as above.  Two or more workgroups
-// share a CU, so one's waits, barriers and epilogue pass under the others'
-// copies.  Blocks of 16 rows that the m-tile does not have are left out: the
-// loop is built for each number of them (in steps of a quarter), so that it has
-// no branch and reads all its fragments before it multiplies (with branches
-// and one fragment at a time linear 1000 x 6144 x 1792 took 27 us, now 19).
-// It copies the rows half as often per weight as the kernel above, and is ahead
-// where these count: gate/up of 96 experts, 43 rows each, 387 against 433 us.
-template <int MT, int NT, int WM, int WN, int WGS, bool DUAL, typename OUT>
+// Between those and the tiles of gemm_dma.h: MT rows x NT channels (DUAL: half
+// of them gate, half up), whose operands WM x WN waves share in LDS, in chunks
+// of 128 codes of k; a wave has MT / WM rows and NT / WN channels.  Swizzle and
+// fragments as above.  The tokens of a chunk, which come from the cache, are
+// copied one chunk ahead, its weights, which come from HBM, SW - 1 chunks (128
+// x 128, gate/up of 96 experts, 63 rows each: SW = 2 428 us, SW = 3 408).  Small
+// tiles have two or three workgroups on a CU, so one's waits, barriers and
+// epilogue pass under the others' copies; the largest fills the CU's LDS with
+// one workgroup of eight waves, which copies least per product.  Blocks of 16
+// rows that the m-tile does not have are left out: the loop is built for each
+// number of them (in steps of a quarter), so that it has no branch and reads all
+// its fragments before it multiplies (with branches and one fragment at a time
+// linear 1000 x 6144 x 1792 took 27 us, now 20), and tokens that are not there
+// are not copied.  Rows are copied half as often per weight as by the kernel
+// above: gate/up of 96 experts, 43 rows each, 387 against 433 us.
+template <int MT, int NT, int WM, int WN, int WGS, int SW, bool DUAL, typename OUT>
 __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params p) {
   using namespace dma;
   constexpr int OC = DUAL ? NT / 2 : NT, W = WM * WN;
   constexpr int MB = MT / WM / 16, NB = NT / WN / 16;  // a wave's blocks of 16 rows and 16 channels
-  constexpr int STAGE = (MT + NT) * 128;
+  constexpr int WST = NT * 128, XST = MT * 128;        // bytes of a chunk: weight rows, token rows
   constexpr int CW = NT / 8 / W, CX = MT / 8 / W;      // copies per wave and chunk: of weight rows, of token rows
-  constexpr int PER = CW + CX;
   constexpr int KB = NB * MB > 16 ? 1 : 2;             // k-steps whose fragments are read at once
-  static_assert(CW % 2 == 0 && NB % 2 == 0 && CX >= 1, "shares of the copies; gate and up blocks");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+  static_assert(CW % 2 == 0 && CW * 8 * W == NT && CX * 8 * W == MT && NB % 2 == 0, "shares of the copies; gate and up blocks");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[SW * WST + 2 * XST];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -613,41 +616,58 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
     const i32x4 rw2 = DUAL ? make_rsrc(p.w2 + ((int64_t)g * p.N + n0) * p.ldw, (uint64_t)nlim * p.ldw) : rw;
     const i32x4 rx = p.row_token ? make_rsrc(p.x, (uint64_t)p.x_rows * p.ldx)
                                  : make_rsrc(p.x + (int64_t)m0 * p.ldx, (uint64_t)mlim * p.ldx);
-    // A wave copies four times 8 of the weight rows, then its share of the
-    // token rows.  With DUAL a wave's channel blocks are gate, up, gate, up ..:
+    // A wave copies CW times 8 of the weight rows, and of the token rows every
+    // W-th eight.  With DUAL a wave's channel blocks are gate, up, gate, up ..:
     // LDS weight row r is gate or up by bit 4, channel 16 (r / 32) + r % 16.
-    uint32_t v[PER];
-    auto row8 = [&](int j) { return j < CW ? 8 * (wave * CW + j) : NT + 8 * (wave * CX + j - CW); };
-    auto piece = [&](int j) { return ((lane & 7) ^ swz16(row8(j) + (lane >> 3))) << 4; };
+    uint32_t vw[CW], vx[CX];
+    auto row_w = [&](int j) { return 8 * (wave * CW + j); };
+    auto row_x = [&](int j) { return 8 * (wave + W * j); };
+    auto piece = [&](int row8) { return ((lane & 7) ^ swz16(row8 + (lane >> 3))) << 4; };
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int row = row8(j) + (lane >> 3);
-      if (j < CW) {
-        const int src = DUAL ? (row >> 5) * 16 + (row & 15) : row;
-        v[j] = src < nlim ? (uint32_t)(src * p.ldw) + piece(j) : 0x80000000u;
-      } else {
-        const int m = row - NT;
-        uint32_t src = m;
-        if (p.row_token && m < mlim) src = p.row_token[m0 + m];
-        v[j] = m < mlim ? (uint32_t)(src * p.ldx) + piece(j) : 0x80000000u;
-      }
+    for (int j = 0; j < CW; ++j) {
+      const int row = row_w(j) + (lane >> 3), src = DUAL ? (row >> 5) * 16 + (row & 15) : row;
+      vw[j] = src < nlim ? (uint32_t)(src * p.ldw) + piece(row_w(j)) : 0x80000000u;
+    }
+#pragma unroll
+    for (int j = 0; j < CX; ++j) {
+      const int row = row_x(j) + (lane >> 3);
+      uint32_t src = row;
+      if (p.row_token && row < mlim) src = p.row_token[m0 + row];
+      vx[j] = row < mlim ? (uint32_t)(src * p.ldx) + piece(row_x(j)) : 0x80000000u;
     }
     const int chunks = (p.K + 127) / 128;
     const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
-    auto copy_as = [&](int i, auto tail_c) {  // (TAIL as above)
-      const uint32_t st = lds + (uint32_t)(i & 1) * STAGE;
+    // Chunk i's weights to ring stage i % SW, its tokens to i % 2 (TAIL as
+    // above).  Eights of token rows that the m-tile does not have are left as
+    // they are: nothing is stored of their products.
+    auto copy_w_as = [&](int i, auto tail_c) {
+      const uint32_t st = lds + (uint32_t)(i % SW) * WST;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        uint32_t o = v[j];
-        if (decltype(tail_c)::value && i * 128 + piece(j) >= p.K) o = 0x80000000u;
+      for (int j = 0; j < CW; ++j) {
+        uint32_t o = vw[j];
+        if (decltype(tail_c)::value && i * 128 + piece(row_w(j)) >= p.K) o = 0x80000000u;
         // (with DUAL bit 4 of an LDS weight row is a bit of j, or of the wave when it copies two times 8 rows)
-        const i32x4 r = j >= CW ? rx : (DUAL && (CW == 2 ? wave & 1 : j & 2) ? rw2 : rw);
-        dma16(r, o, (uint32_t)(i * 128), __builtin_amdgcn_readfirstlane(st + row8(j) * 128));
+        const i32x4 r = DUAL && (CW == 2 ? wave & 1 : j & 2) ? rw2 : rw;
+        dma16(r, o, (uint32_t)(i * 128), __builtin_amdgcn_readfirstlane(st + row_w(j) * 128));
       }
     };
-    auto copy = [&](int i) {
-      if (i * 128 + 128 <= p.K) copy_as(i, std::false_type());
-      else copy_as(i, std::true_type());
+    auto copy_x_as = [&](int i, auto tail_c) {
+      const uint32_t st = lds + SW * WST + (uint32_t)(i & 1) * XST;
+#pragma unroll
+      for (int j = 0; j < CX; ++j) {
+        if (row_x(j) >= mlim) break;
+        uint32_t o = vx[j];
+        if (decltype(tail_c)::value && i * 128 + piece(row_x(j)) >= p.K) o = 0x80000000u;
+        dma16(rx, o, (uint32_t)(i * 128), __builtin_amdgcn_readfirstlane(st + row_x(j) * 128));
+      }
+    };
+    auto copy_w = [&](int i) {
+      if (i * 128 + 128 <= p.K) copy_w_as(i, std::false_type());
+      else if (i < chunks) copy_w_as(i, std::true_type());
+    };
+    auto copy_x = [&](int i) {
+      if (i * 128 + 128 <= p.K) copy_x_as(i, std::false_type());
+      else if (i < chunks) copy_x_as(i, std::true_type());
     };
 
     // The tile's row blocks go to the wave rows in turn; a wave's that exist:
@@ -675,10 +695,14 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
     // first MBA row blocks.
     auto step = [&](int i, auto mba_c, auto tail_c) {
       constexpr int MBA = decltype(mba_c)::value;
-      wait_vm<0>();
+      // (the last copies asked for, the weights of chunk i + SW - 2, may be on their way still)
+      if (SW > 2 && i + SW - 2 < chunks) wait_vm<CW>();
+      else wait_vm<0>();
       lds_barrier();  // chunk i has landed for every wave, and every wave has read chunk i - 1
-      if (i + 1 < chunks) copy(i + 1);
-      const uint8_t* st = smem + (i & 1) * STAGE;
+      copy_x(i + 1);
+      copy_w(i + SW - 1);
+      const uint8_t* st = smem + (uint32_t)(i % SW) * WST;
+      const uint8_t* stx = smem + SW * WST + (i & 1) * XST;
 #pragma unroll
       for (int k = 0; k < 2; k += KB) {
         i32x4_t fw[KB][NB], fx[KB][MBA > 0 ? MBA : 1];
@@ -694,8 +718,8 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
           }
 #pragma unroll
           for (int b = 0; b < MBA; ++b) {
-            const int r = NT + (b * WM + wm) * 16 + (lane & 15);
-            fx[kk][b] = *reinterpret_cast<const i32x4_t*>(st + r * 128 + (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
+            const int r = (b * WM + wm) * 16 + (lane & 15);
+            fx[kk][b] = *reinterpret_cast<const i32x4_t*>(stx + r * 128 + (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
           }
         }
 #pragma unroll
@@ -713,7 +737,10 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
       for (int i = 0; i < plain; ++i) step(i, mba_c, std::false_type());
       if (tail) step(plain, mba_c, std::true_type());
     };
-    copy(0);
+    copy_w(0);
+    copy_x(0);
+#pragma unroll
+    for (int i = 1; i < SW - 1; ++i) copy_w(i);
     constexpr int Q = (MB + 3) / 4;  // a loop for each number of row blocks, in steps of a quarter of all
     switch ((blocks + Q - 1) / Q) {
       case 0: loop(std::integral_constant<int, 0>()); break;
@@ -735,7 +762,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
   }
 }
 
-template <int MT, int NT, int WM, int WN, int WGS, bool DUAL, typename OUT>
+template <int MT, int NT, int WM, int WN, int WGS, int SW, bool DUAL, typename OUT>
 hipError_t run_mid(I8Params p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
   // One m-tile per group: nothing shares its weights, so its rows are kept
   // together (gate/up, 105 rows each: 476 us against 515 by channel tiles).
@@ -743,7 +770,7 @@ hipError_t run_mid(I8Params p, int64_t rows, int64_t groups, int64_t mean, hipSt
   const int64_t slots = p.offsets ? rows / MT + std::min<int64_t>(p.ngroups, rows) : cdiv(rows, MT);
   p.tiles = tile_count(p, slots, cdiv(p.N, DUAL ? NT / 2 : NT));
   const unsigned grid = (unsigned)std::min<int64_t>(p.tiles, 1 << 22);
-  i8_mid_rows_kernel<MT, NT, WM, WN, WGS, DUAL, OUT><<<grid, 64 * WM * WN, 0, s>>>(p);
+  i8_mid_rows_kernel<MT, NT, WM, WN, WGS, SW, DUAL, OUT><<<grid, 64 * WM * WN, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -763,10 +790,22 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
 // evenly spread routing (a skewed one is computed as well, in more m-tiles).
 // Times of gate/up of 96 experts, K = 6144, N = 2 x 1792, unless said otherwise.
 //   - From 33 rows on the shared-operand kernel, where its tiles fill the chip:
-//     64 rows a tile up to 48 (43 rows each: 387 us; 128 rows a tile 414), then
-//     192 where a group has one such tile and 128 would be two (171 rows: 579
-//     us against 709), else 128 (63 rows: 430 us, 192 rows a tile 443; linear
-//     4096 x 2048 x 2048: 25 us, 192 rows a tile 32, 64 rows 31).
+//     64 rows a tile up to 48 (43 rows each: 392 us; 128 rows a tile 398) or
+//     where 128 would be too few (linear 2000 x 2048 x 2048, 256 tiles of 128:
+//     21.6 us, 64 rows 17.6), else 128 (63 rows: 408 us; 64 rows a tile 484).
+//   - Where one taller tile saves a second of 128 rows: for gate/up 256 x 256
+//     with one workgroup a CU, which also has room for the busiest expert's
+//     rows, from 81 rows (105 rows each: 446 us, 128 x 128 468; 64 experts of 125
+//     rows, K = 2048: 61.0 and 77.5), its waves as 4 x 2 from 129 (171 rows: 521,
+//     2 x 4 543, 128 x 128 727; 105 rows: 452); for a single product 192 x 128
+//     (down of 64 experts, K = 1024, 125 rows each: 42.2 us, 256 x 256 43.8, 128 x
+//     128 50.8), also for very many rows (linear 6144 x 4096 x 4096, 1024 tiles:
+//     107 us, 128 x 128 120; 4096 x 4096 x 4096, 704 tiles: 86 and 81).
+//     As few tiles of 64 x 128 are still ahead of the kernel of few rows: 250 of
+//     groups (24 experts, K = 832, 125 rows, 336 tiles: 11.6 us, 64 x 64 of that
+//     kernel 16.5; 8 experts, K = 1024, 250 rows, 256 tiles: 11.1 and 12.7), 400 of a
+//     linear layer (512 x 6144 x 6144, 384 tiles: 35.4 and 34.2; 768 rows: 45 and
+//     52; 1000 x 2048 x 1024, 256 tiles: 9.7 and 8.6).
 //   - A short K (a wave's share of it ends before its copies have got going)
 //     and many tiles: its 64-row tiles with fewer rows too (down, K = 1792, 3 of 10
 //     experts one row each: 46 us against 51).
@@ -782,11 +821,19 @@ template <bool DUAL, typename OUT>
 hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean, hipStream_t s) {
   const int64_t N = DUAL ? 2 * (int64_t)p.N : p.N;
   auto tiles = [&](int mt, int nt) { return groups * cdiv(mean, mt) * cdiv(N, nt); };
-  if (mean > 104 && mean <= 176 && tiles(192, 128) >= 400)
-    return run_mid<192, 128, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
-  if (mean > 48 && tiles(128, 128) >= 400) return run_mid<128, 128, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
-  if (mean > 32 ? tiles(64, 128) >= 512 : p.K <= 2048 && tiles(64, 128) >= 1200)
-    return run_mid<64, 128, 1, 4, 3, DUAL, OUT>(p, rows, groups, mean, s);
+  if constexpr (DUAL) {
+    if (mean > 80 && mean <= 224 && tiles(256, 256) >= 240) {
+      if (mean <= 128) return run_mid<256, 256, 2, 4, 1, 3, DUAL, OUT>(p, rows, groups, mean, s);
+      return run_mid<256, 256, 4, 2, 1, 3, DUAL, OUT>(p, rows, groups, mean, s);
+    }
+  } else {
+    if ((mean > 104 && mean <= 176 && tiles(192, 128) >= 400) || (mean >= 1024 && tiles(192, 128) >= 800))
+      return run_mid<192, 128, 2, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
+  }
+  if (mean > 48 && tiles(128, 128) >= 400) return run_mid<128, 128, 2, 2, 2, 3, DUAL, OUT>(p, rows, groups, mean, s);
+  const int64_t fill64 = p.offsets ? 250 : 400;
+  if (mean > 32 ? tiles(64, 128) >= fill64 : p.K <= 2048 && tiles(64, 128) >= 1200)
+    return run_mid<64, 128, 1, 4, 3, 2, DUAL, OUT>(p, rows, groups, mean, s);
   constexpr int64_t FILL = 300;
   if (mean > 32 && tiles(64, 64) >= FILL) return run_few<4, 4, 4, 2, DUAL, OUT>(p, rows, s);
   if (mean > 8) {
@@ -801,15 +848,31 @@ hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean,
   return run_few<1, 2, 4, 4, DUAL, OUT>(p, rows, s);
 }
 
-// Whether a product goes to the 256 x 256 tiles (whole k-tiles of 128 codes, at
-// least four) instead of the kernels above.  They are ahead where there are
-// many (they run on one workgroup per CU, round by round) and groups have many
-// rows, or K is short: gate/up 171 rows each 595 us against 579, 250 rows 699
-// and 857; down (K = 1792) 43 rows 262 and 237, 63 rows 268 and 272, 105 rows 286
-// and 321; down of 64 experts, K = 1024, 125 rows, 512 tiles: 51 and 43; linear
-// 4096 x 6144 x 6144, 384 tiles: 169 and 158; 16384 rows, 1536: 519 and 638.
-bool use_tiles(int64_t K, int64_t tiles, int64_t mean) {
-  return K % 128 == 0 && K >= 512 && (mean > 176 || (K <= 2048 && mean > 56 && tiles >= 1024));
+// Whether a product goes to the tiles of gemm_dma.h (whole k-tiles of 128 codes,
+// at least four) instead of the kernels above.  They run on one workgroup per CU,
+// round by round, and for the experts they are ahead where there are some rounds
+// of them (down of 8 experts, K = 8192, 500 rows each, 256 tiles: 191 us against
+// 177; of 16, K = 2048, 512 tiles: 93 and 107) and groups have many rows (gate/up 206
+// rows each 454 us against 439, 229 rows 624 and 612, 250 rows 704 and 761; down
+// of K = 1536 206 rows 276 and 311); for down also where K is short and they are
+// very many (K = 1792, 43 rows each 262 and 241, 63 rows 269 and 274, 105 rows 284
+// and 324; gate/up, K = 2048, 83 rows, 1344 tiles: 207 and 162).
+bool use_tiles(int64_t K, int64_t tiles, int64_t mean, bool dual) {
+  if (K % 128 || K < 512) return false;
+  return (mean > (dual ? 224 : 176) && tiles >= 400) || (!dual && K <= 2048 && mean > 56 && tiles >= 1024);
+}
+
+// The same for a linear layer, whose tiles are all whole ones but the last: how
+// full the rounds are decides.  One round (K = 6144: 192 tiles 80 us against 90,
+// 224 tiles 86 and 108; K = 2048, 256 tiles: 47 and 54; K = 1024: 35 and 35) or
+// three (8192 x 4608 x 4096, 576 tiles: 160 and 177) from three quarters; two want
+// more (K = 6144, 384 tiles: 169 and 158, 480 tiles 168 and 189); with a short K
+// from four (K = 512, 768 tiles: 54 and 66; 256 tiles: 30 and 25).
+bool use_tiles_linear(int64_t K, int64_t tiles) {
+  if (K % 128 || K < 512) return false;
+  const int64_t cus = num_cus(), rounds = cdiv(tiles, cus);
+  if (rounds > 3 || (rounds == 3 && tiles == 3 * cus)) return true;
+  return K >= 2048 && 100 * tiles >= (rounds == 2 ? 84 : 75) * rounds * cus;
 }
 
 // The local experts that have rows, as expected: a token's picks fall on num_local of E experts.
@@ -849,7 +912,7 @@ hipError_t launch_gate_up_i8(const moe_desc& d, const int32_t* offsets, const in
   p.ldy = d.f;
   p.gu = reinterpret_cast<uint16_t*>(gu);
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
-  if (use_tiles(d.d, d.num_local * cdiv(mean, 256) * cdiv(d.f, 128), mean))
+  if (use_tiles(d.d, d.num_local * cdiv(mean, 256) * cdiv(d.f, 128), mean, true))
     return launch_gate_up_i8_tiles(d, offsets, row_token, xq, xs, W1q, W1s, W3q, W3s, gu, h, s);
   return run_i8<true, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
@@ -870,7 +933,7 @@ hipError_t launch_down_i8(const moe_desc& d, const int32_t* offsets, const int8_
   p.y = y_perm;
   p.ldy = d.d;
   const int64_t mean = cdiv((int64_t)d.T * d.k, d.E);
-  if (use_tiles(d.f, d.num_local * cdiv(mean, 256) * cdiv(d.d, 256), mean))
+  if (use_tiles(d.f, d.num_local * cdiv(mean, 256) * cdiv(d.d, 256), mean, false))
     return launch_down_i8_tiles(d, offsets, hq, hs, W2q, W2s, y_perm, s);
   return run_i8<false, uint16_t>(p, (int64_t)d.T * std::min(d.k, d.num_local), hit_experts(d), mean, s);
 }
@@ -896,7 +959,7 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
   const int64_t esz = dtype == MOE_BF16 ? 2 : 4;
   // (the tiles store their output rows as 16-byte vectors)
   const int64_t tiles = cdiv(M, 256) * cdiv(N, 256);
-  if (N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 && tiles >= 768 && use_tiles(K, tiles, M))
+  if (N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 && use_tiles_linear(K, tiles))
     return launch_i8_linear_tiles((int)M, (int)N, (int)K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, s);
   if (dtype == MOE_BF16) return run_i8<false, uint16_t>(p, M, 1, M, s);
   return run_i8<false, float>(p, M, 1, M, s);

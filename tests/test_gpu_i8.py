@@ -126,7 +126,8 @@ def _linear(gpu, M, N, K, dtype, bias, pad=0, seed=0, codes=None):
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 16, 16), (1, 3, 17), (2, 64, 128), (15, 63, 127), (16, 65, 129), (17, 1003, 1990),
                                    (31, 32, 33), (33, 48, 512), (63, 128, 640), (64, 64, 64), (65, 100, 1000), (1, 3584, 6144),
                                    (130, 260, 1024), (257, 257, 1024), (300, 520, 2048), (1000, 777, 1537), (513, 1024, 6144),
-                                   (500, 2500, 100), (1500, 3150, 100), (2600, 2601, 130), (8200, 6144, 512)])
+                                   (500, 2500, 100), (1500, 3150, 100), (2600, 2601, 130), (8200, 6144, 512), (2040, 6136, 2048),
+                                   (1100, 23000, 100)])
 def test_linear_matches_the_oracle(gpu, M, N, K, dtype, bias):
     _linear(gpu, M, N, K, dtype, bias)
 
@@ -225,6 +226,9 @@ SHAPES = {  # T, d, f, E, k, e0, NL, skew
     "75 rows, many tiles": (600, 832, 448, 64, 8, 0, 64, 0.0),
     "125 rows, many tiles": (1000, 832, 448, 64, 8, 0, 64, 0.0),
     "125 rows, skewed": (1000, 832, 448, 64, 8, 0, 64, 1.0),
+    "180 rows, many tiles": (1440, 832, 448, 64, 8, 0, 64, 0.0),
+    "180 rows, skewed": (1440, 832, 448, 64, 8, 0, 64, 0.6),
+    "about 330 rows, many tiles": (1300, 1792, 1024, 32, 8, 0, 32, 0.3),
     "500 rows, K no multiple of 128": (2000, 832, 448, 32, 8, 0, 32, 0.3),
 }
 
