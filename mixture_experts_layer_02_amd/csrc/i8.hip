@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
   constexpr int WST = NT * 128, XST = MT * 128;        // bytes of a chunk: weight rows, token rows
   constexpr int CW = NT / 8 / W, CX = MT / 8 / W;      // copies per wave and chunk: of weight rows, of token rows
   constexpr int KB = NB * MB > 16 ? 1 : 2;             // k-steps whose fragments are read at once
+  constexpr bool PIPE = DUAL && WGS == 1;                    // (see pipe)
+  static_assert(!PIPE || (SW > 2 && NB % 4 == 0), "stages and halves of pipe");
   static_assert(CW % 2 == 0 && CW * 8 * W == NT && CX * 8 * W == MT && NB % 2 == 0, "shares of the copies; gate and up blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SW * WST + 2 * XST];
 
@@ -683,13 +685,16 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
     auto c_out = [&](int a) { return (wn * NB + a) * (DUAL ? 8 : 16) + (lane >> 4) * 4; };
     Channels ch[NB / AS];
     float sx[MB];
+    auto scales = [&]() {
 #pragma unroll
-    for (int a = 0; a < NB; a += AS) ch[a / AS].template load<DUAL>(p, g, n0 + c_out(a));
+      for (int a = 0; a < NB; a += AS) ch[a / AS].template load<DUAL>(p, g, n0 + c_out(a));
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int row = (b * WM + wm) * 16 + (lane & 15);
-      sx[b] = row < mlim ? p.sx[p.row_token ? p.row_token[m0 + row] : m0 + row] : 0.f;
-    }
+      for (int b = 0; b < MB; ++b) {
+        const int row = (b * WM + wm) * 16 + (lane & 15);
+        sx[b] = row < mlim ? p.sx[p.row_token ? p.row_token[m0 + row] : m0 + row] : 0.f;
+      }
+    };
+    if (!PIPE) scales();
 
     // Chunk i: the next one's copies, its fragments, its products with the
     // first MBA row blocks.
@@ -731,16 +736,82 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
               acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[kk][a], fx[kk][b], acc[a][b], 0, 0, 0);
       }
     };
+    // PIPE: one workgroup on the CU, so its fragments are read while it
+    // multiplies: a chunk goes in four parts, by k-step and half of the channel
+    // blocks, and each part's products pass under the next part's reads, the
+    // last one's under the next chunk's, so the barrier between chunks lies
+    // before the last part: there every wave has read the whole chunk, and the
+    // copies into its stages start.
+    auto pipe = [&](auto mba_c) {
+      constexpr int MBA = decltype(mba_c)::value, M1 = MBA > 0 ? MBA : 1, HB = MBA > 0 ? NB / 2 : 0;
+      i32x4_t x0[M1], x1[M1], wa[NB / 2], wb[NB / 2];
+      auto at = [&](const uint8_t* s, int r, int ks) {
+        return *reinterpret_cast<const i32x4_t*>(s + r * 128 + (((4 * ks + (lane >> 4)) ^ swz16(r)) << 4));
+      };
+      auto read_x = [&](i32x4_t (&f)[M1], int i, int ks) {
+        const uint8_t* s = smem + SW * WST + (i & 1) * XST;
+#pragma unroll
+        for (int b = 0; b < MBA; ++b) f[b] = at(s, (b * WM + wm) * 16 + (lane & 15), ks);
+      };
+      auto read_w = [&](i32x4_t (&f)[NB / 2], int i, int ks, int half) {
+        const uint8_t* s = smem + (uint32_t)(i % SW) * WST;
+#pragma unroll
+        for (int a = 0; a < HB; ++a) f[a] = at(s, (wn * NB + half * (NB / 2) + a) * 16 + (lane & 15), ks);
+      };
+      auto mul = [&](const i32x4_t (&w)[NB / 2], const i32x4_t (&x)[M1], auto half_c) {
+        constexpr int A0 = decltype(half_c)::value * (NB / 2);
+#pragma unroll
+        for (int a = 0; a < HB; ++a)
+#pragma unroll
+          for (int b = 0; b < MBA; ++b)
+            acc[A0 + a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[a], x[b], acc[A0 + a][b], 0, 0, 0);
+      };
+      const std::integral_constant<int, 0> h0;
+      const std::integral_constant<int, 1> h1;
+      read_x(x0, 0, 0);
+      read_w(wa, 0, 0, 0);
+      for (int i = 0; i < chunks; ++i) {
+        read_w(wb, i, 0, 1);
+        mul(wa, x0, h0);
+        read_x(x1, i, 1);
+        read_w(wa, i, 1, 0);
+        mul(wb, x0, h1);
+        read_w(wb, i, 1, 1);
+        mul(wa, x1, h0);
+        if (i + 1 < chunks) {
+          // (the last copies asked for, the weights of chunk i + SW - 1, may be on their way still)
+          if (i + SW - 1 < chunks) wait_vm<CW>();
+          else wait_vm<0>();
+          lds_barrier();  // chunk i + 1 has landed for every wave, and every wave has read chunk i
+          copy_x(i + 2);
+          copy_w(i + SW);
+          read_x(x0, i + 1, 0);
+          read_w(wa, i + 1, 0, 0);
+        }
+        mul(wb, x1, h1);
+      }
+    };
     const bool tail = p.K % 16 != 0;  // the last chunk needs the mask
     const int plain = tail ? chunks - 1 : chunks;
     auto loop = [&](auto mba_c) {
+      if constexpr (PIPE) return pipe(mba_c);
       for (int i = 0; i < plain; ++i) step(i, mba_c, std::false_type());
       if (tail) step(plain, mba_c, std::true_type());
     };
-    copy_w(0);
-    copy_x(0);
+    if constexpr (PIPE) {
+      copy_x(0);
+      copy_x(1);
 #pragma unroll
-    for (int i = 1; i < SW - 1; ++i) copy_w(i);
+      for (int i = 0; i < SW; ++i) copy_w(i);
+      if (SW <= chunks) wait_vm<(SW - 1) * CW>();
+      else wait_vm<0>();
+      lds_barrier();
+    } else {
+      copy_w(0);
+      copy_x(0);
+#pragma unroll
+      for (int i = 1; i < SW - 1; ++i) copy_w(i);
+    }
     constexpr int Q = (MB + 3) / 4;  // a loop for each number of row blocks, in steps of a quarter of all
     switch ((blocks + Q - 1) / Q) {
       case 0: loop(std::integral_constant<int, 0>()); break;
@@ -749,6 +820,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
       case 3: loop(std::integral_constant<int, MB < 3 * Q ? MB : 3 * Q>()); break;
       default: loop(std::integral_constant<int, MB>()); break;
     }
+    if (PIPE) scales();
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       const int row = (b * WM + wm) * 16 + (lane & 15);
@@ -795,9 +867,9 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
 //     21.6 us, 64 rows 17.6), else 128 (63 rows: 408 us; 64 rows a tile 484).
 //   - Where one taller tile saves a second of 128 rows: for gate/up 256 x 256
 //     with one workgroup a CU, which also has room for the busiest expert's
-//     rows, from 81 rows (105 rows each: 446 us, 128 x 128 468; 64 experts of 125
-//     rows, K = 2048: 61.0 and 77.5), its waves as 4 x 2 from 129 (171 rows: 521,
-//     2 x 4 543, 128 x 128 727; 105 rows: 452); for a single product 192 x 128
+//     rows, from 81 rows (105 rows each: 441 us, 128 x 128 472; 171 rows: 523 and
+//     725; 209 rows: 563 and 779; 64 experts of 125 rows, K = 2048: 61.1 and
+//     77.5); for a single product 192 x 128
 //     (down of 64 experts, K = 1024, 125 rows each: 42.2 us, 256 x 256 43.8, 128 x
 //     128 50.8), also for very many rows (linear 6144 x 4096 x 4096, 1024 tiles:
 //     107 us, 128 x 128 120; 4096 x 4096 x 4096, 704 tiles: 86 and 81).
@@ -822,10 +894,8 @@ hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean,
   const int64_t N = DUAL ? 2 * (int64_t)p.N : p.N;
   auto tiles = [&](int mt, int nt) { return groups * cdiv(mean, mt) * cdiv(N, nt); };
   if constexpr (DUAL) {
-    if (mean > 80 && mean <= 224 && tiles(256, 256) >= 240) {
-      if (mean <= 128) return run_mid<256, 256, 2, 4, 1, 3, DUAL, OUT>(p, rows, groups, mean, s);
+    if (mean > 80 && mean <= 224 && tiles(256, 256) >= 240)
       return run_mid<256, 256, 4, 2, 1, 3, DUAL, OUT>(p, rows, groups, mean, s);
-    }
   } else {
     if ((mean > 104 && mean <= 176 && tiles(192, 128) >= 400) || (mean >= 1024 && tiles(192, 128) >= 800))
       return run_mid<192, 128, 2, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
