@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
   constexpr int WST = NT * 128, XST = MT * 128;        // bytes of a chunk: weight rows, token rows
   constexpr int CW = NT / 8 / W, CX = MT / 8 / W;      // copies per wave and chunk: of weight rows, of token rows
   constexpr int KB = NB * MB > 16 ? 1 : 2;             // k-steps whose fragments are read at once
-  constexpr bool PIPE = DUAL && WGS == 1;                    // (see pipe)
+  constexpr bool PIPE = DUAL && WGS == 1;               // (see pipe)
   static_assert(!PIPE || (SW > 2 && NB % 4 == 0), "stages and halves of pipe");
   static_assert(CW % 2 == 0 && CW * 8 * W == NT && CX * 8 * W == MT && NB % 2 == 0, "shares of the copies; gate and up blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SW * WST + 2 * XST];
