@@ -871,8 +871,9 @@ hipError_t run_few(I8Params p, int64_t rows, hipStream_t s) {
 //     725; 209 rows: 563 and 779; 64 experts of 125 rows, K = 2048: 61.1 and
 //     77.5); for a single product 192 x 128
 //     (down of 64 experts, K = 1024, 125 rows each: 42.2 us, 256 x 256 43.8, 128 x
-//     128 50.8), also for very many rows (linear 6144 x 4096 x 4096, 1024 tiles:
-//     107 us, 128 x 128 120; 4096 x 4096 x 4096, 704 tiles: 86 and 81).
+//     128 50.8; linear 300 x 49152 x 4096: 83 us, 128 x 128 104; 180 rows: 52 and 65;
+//     6144 x 4096 x 4096, 1024 tiles: 107 and 120; 512 x 24576 x 6144, 576 tiles:
+//     106 and 103).
 //     As few tiles of 64 x 128 are still ahead of the kernel of few rows: 250 of
 //     groups (24 experts, K = 832, 125 rows, 336 tiles: 11.6 us, 64 x 64 of that
 //     kernel 16.5; 8 experts, K = 1024, 250 rows, 256 tiles: 11.1 and 12.7), 400 of a
@@ -897,7 +898,8 @@ hipError_t run_i8(const I8Params& p, int64_t rows, int64_t groups, int64_t mean,
     if (mean > 80 && mean <= 224 && tiles(256, 256) >= 240)
       return run_mid<256, 256, 4, 2, 1, 3, DUAL, OUT>(p, rows, groups, mean, s);
   } else {
-    if ((mean > 104 && mean <= 176 && tiles(192, 128) >= 400) || (mean >= 1024 && tiles(192, 128) >= 800))
+    if (p.offsets ? mean > 104 && mean <= 176 && tiles(192, 128) >= 400
+                  : mean > 128 && tiles(192, 128) >= (mean <= 192 ? 360 : 700))
       return run_mid<192, 128, 2, 2, 2, 2, DUAL, OUT>(p, rows, groups, mean, s);
   }
   if (mean > 48 && tiles(128, 128) >= 400) return run_mid<128, 128, 2, 2, 2, 3, DUAL, OUT>(p, rows, groups, mean, s);
@@ -932,17 +934,19 @@ bool use_tiles(int64_t K, int64_t tiles, int64_t mean, bool dual) {
   return (mean > (dual ? 224 : 176) && tiles >= 400) || (!dual && K <= 2048 && mean > 56 && tiles >= 1024);
 }
 
-// The same for a linear layer, whose tiles are all whole ones but the last: how
-// full the rounds are decides.  One round (K = 6144: 192 tiles 80 us against 90,
-// 224 tiles 86 and 108; K = 2048, 256 tiles: 47 and 54; K = 1024: 35 and 35) or
-// three (8192 x 4608 x 4096, 576 tiles: 160 and 177) from three quarters; two want
-// more (K = 6144, 384 tiles: 169 and 158, 480 tiles 168 and 189); with a short K
-// from four (K = 512, 768 tiles: 54 and 66; 256 tiles: 30 and 25).
-bool use_tiles_linear(int64_t K, int64_t tiles) {
+// The same for a linear layer: what decides is how much of the rounds its rows
+// and channels fill, tiles that are not whole counted by what they have.  One
+// round (K = 6144: 0.75 full 80 us against 90, 0.85 86 and 108; K = 2048, full: 47
+// and 54; K = 4096, 256 rows, 0.75 65 and 75, 180 rows, 0.53 62 and 52, 128 rows 59
+// and 40) or three (8192 x 4608 x 4096, 0.75: 160 and 177) from three quarters; two
+// want more (K = 6144: 0.75 169 and 158, 0.92 168 and 189; K = 4096, 300 x 49152,
+// 0.44: 116 and 83); a short K three full ones (K = 512, 3 rounds: 54 and 66, one 30
+// and 25).
+bool use_tiles_linear(int64_t M, int64_t N, int64_t K) {
   if (K % 128 || K < 512) return false;
-  const int64_t cus = num_cus(), rounds = cdiv(tiles, cus);
-  if (rounds > 3 || (rounds == 3 && tiles == 3 * cus)) return true;
-  return K >= 2048 && 100 * tiles >= (rounds == 2 ? 84 : 75) * rounds * cus;
+  const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), rounds = cdiv(tiles, num_cus());
+  const double full = (double)M * (double)N / ((double)rounds * num_cus() * 65536.0);
+  return full >= (rounds == 2 ? 0.84 : 0.72) && (K >= 2048 || tiles >= 3 * num_cus());
 }
 
 // The local experts that have rows, as expected: a token's picks fall on num_local of E experts.
@@ -1028,8 +1032,7 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
   p.ldy = ldy;
   const int64_t esz = dtype == MOE_BF16 ? 2 : 4;
   // (the tiles store their output rows as 16-byte vectors)
-  const int64_t tiles = cdiv(M, 256) * cdiv(N, 256);
-  if (N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 && use_tiles_linear(K, tiles))
+  if (N * esz % 16 == 0 && ldy * esz % 16 == 0 && ldy <= 1 << 20 && use_tiles_linear(M, N, K))
     return launch_i8_linear_tiles((int)M, (int)N, (int)K, xq, ldx, xs, wq, ldw, ws, bias, y, ldy, dtype, s);
   if (dtype == MOE_BF16) return run_i8<false, uint16_t>(p, M, 1, M, s);
   return run_i8<false, float>(p, M, 1, M, s);
