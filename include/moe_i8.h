@@ -37,7 +37,8 @@ int moe_i8_quantize_rows(const void* w, int dtype, int64_t rows, int64_t cols, i
 /* A linear layer on INT8 codes (e.g. a dense projection beside the experts):
  *   y[m][n] = xs[m] ws[n] (sum over k of xq[m][k] wq[n][k]) + bias[n]
  *   with the sum in 32-bit integers (exact), then, in float32 and in this order,
- *   times xs, times ws, plus the bias, and one rounding to y's type.
+ *   times xs, times ws, plus the bias, each rounded (no fused operation), and one
+ *   rounding to y's type: a row's values do not depend on the rows beside it.
  *   xq [M][K] codes, rows ldx bytes apart, xs [M]; wq [N][K] codes, rows ldw
  *   bytes apart, ws [N]; bias [N] float32 or NULL; y [M][N] MOE_BF16 or
  *   MOE_F32 as `dtype`, rows ldy >= N elements apart.  Any M >= 0, N >= 1 and

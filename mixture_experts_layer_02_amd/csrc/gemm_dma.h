@@ -1418,6 +1418,8 @@ __global__ void __launch_bounds__(256, 1) gemm_dma_kernel(GemmParams p) {
             const int row = rowb + sl * 8 + rl;  // row in the tile
             const int col = col_base + cv;       // column in the tile
             if constexpr (I8) {
+              // (not fused with the bias' addition below: see moe_i8_linear)
+#pragma clang fp contract(off)
               const float rs = s_rsc[it & 1][row & 255];  // (an inactive block's rows lie past 255 and are not stored)
 #pragma unroll
               for (int q = 0; q < W; ++q) {

@@ -363,6 +363,9 @@ __device__ __forceinline__ void store4(const I8Params& p, int64_t r, int n, floa
       *reinterpret_cast<u32x2_t*>(gr + p.N) = u32x2_t{pack_bf2(up[0], up[1]), pack_bf2(up[2], up[3])};
     }
   } else {
+    // (the product rounded before the bias is added, here and in gemm_dma.h's
+    // epilogue: a row's outputs are the same whichever kernel takes it)
+#pragma clang fp contract(off)
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = (float)s1[q] * sx * ch.s1[q] + ch.b[q];
   }
