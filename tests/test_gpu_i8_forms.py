@@ -3,17 +3,21 @@
 The name of the launched kernel is part of each test, so a moved limit between
 the forms cannot leave one of them without its test.  Outputs that the header
 gives as a sequence of float32 operations are compared bit for bit:
-  linear     fl(fl(fl(fl(S) xs) ws) + b), then one rounding to the output type,
-with S the whole-number sum, taken here in float64, where it is exact.
+  linear     fl(fl(fl(fl(S) xs) ws) + b), then one rounding to the output type;
+  G, U       fl(fl(fl(S) xs) ws), then one rounding to bf16; down likewise;
+with S the whole-number sum, taken here in float64, where it is exact.  h goes
+by the bound of silu(G) U in float32 (see test_gpu_i8).
 """
 import re
 
+import numpy as np
 import pytest
 import torch
 
 import mixture_experts_layer_02_amd as moe
+from gpu_util import to_host
 from launched import kernels
-from test_gpu_i8 import SENTINEL
+from test_gpu_i8 import SENTINEL, U32, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +116,95 @@ def test_linear_of_rows_far_apart_on_shared_tiles(gpu, M, N, ldw, form):
     moe.i8_linear(xq, xs, wq, ws, y[:, :N], bias=b)
     _same(y[:, :N], (_scaled(xq, xs, wq, ws) + b).to(BF))
     assert (y[:, N:N + 256] == SENTINEL).all()
+
+
+EXPERTS = [  # T, d, f, E, k, experts here, the forms of gate/up and of down
+    (1, 4096, 64, 8, 1, 8, ("few", 1, 2, 8), ("few", 1, 2, 4)),
+    (1, 6144, 1792, 384, 8, 96, ("few", 1, 2, 8), ("few", 1, 2, 4)),
+    (2, 6144, 1792, 384, 8, 96, ("few", 1, 2, 8), ("few", 1, 4, 4)),
+    (5, 64, 4160, 8, 1, 8, ("few", 1, 8, 4), ("few", 1, 2, 8)),
+    (3, 832, 448, 24, 8, 24, ("few", 1, 4, 4), ("few", 1, 4, 4)),
+    (60, 576, 1024, 64, 1, 64, ("few", 1, 8, 4), ("few", 1, 8, 4)),
+    (100, 512, 192, 24, 2, 24, ("few", 1, 2, 4), ("few", 2, 2, 4)),
+    (100, 192, 64, 96, 8, 96, ("few", 2, 2, 4), ("few", 2, 2, 4)),
+    (100, 832, 448, 24, 2, 24, ("few", 2, 4, 4), ("few", 2, 4, 4)),
+    (300, 576, 1024, 64, 2, 64, ("few", 2, 8, 4), ("few", 2, 8, 4)),
+    (100, 832, 448, 24, 8, 24, ("few", 4, 4, 4), ("few", 4, 4, 4)),
+    (120, 832, 448, 192, 8, 192, ("mid", 64, 128, 1), ("mid", 64, 128, 1)),
+    (600, 192, 448, 64, 8, 64, ("mid", 128, 128, 2), ("mid", 64, 128, 1)),
+    (400, 832, 448, 64, 8, 64, ("mid", 128, 128, 2), ("mid", 128, 128, 2)),
+    (1300, 576, 448, 96, 8, 96, ("mid", 256, 256, 4), ("mid", 192, 128, 2)),
+    # four k-tiles, the fewest that the large tiles take: the next tile is not loaded ahead
+    (1000, 512, 1792, 32, 8, 32, "tiles", ("mid", 64, 128, 1)),
+    (1300, 512, 1792, 32, 8, 32, "tiles", ("mid", 64, 128, 1)),
+    (1000, 4096, 512, 64, 4, 64, ("mid", 128, 128, 2), "tiles"),
+]
+
+
+def _routed(T, d, f, E, k, NL, dyn):
+    """The routed rows of T tokens with k random picks each, the first token's first pick an expert that is here."""
+    D = moe.make_desc(T, d, f, E, k, 0, NL, "bf16", tile_counters=moe.new_tile_counters() if dyn else None)
+    g = torch.Generator(device="cuda").manual_seed(T + d + f)
+    score = torch.rand(T, E, generator=g, device="cuda")
+    score[0, NL - 1] = 2.0
+    idx = score.topk(k, dim=1).indices.to(torch.int32)
+    b = moe.Buffers(D, gather=True)
+    moe.permute(D, idx, None, b.counts, b.offsets, b.row_token, b.slot_row, None, b.ws_permute)
+    return D, b, b.offsets.tolist(), g
+
+
+def _per_expert(off, rows, rs, wq, ws):
+    out = torch.zeros(off[-1], wq.shape[1], device="cuda")
+    for n in range(len(off) - 1):
+        a, z = off[n], off[n + 1]
+        if z > a:
+            out[a:z] = _scaled(rows[a:z], rs[a:z], wq[n], ws[n])
+    return out
+
+
+def _as_form(form, dyn):
+    return ("tiles", int(dyn)) if form == "tiles" else form
+
+
+CASES = [(*c, dyn) for c in EXPERTS for dyn in ((False, True) if "tiles" in c else (False,))]
+
+
+@pytest.mark.parametrize("T,d,f,E,k,NL,form,_,dyn", CASES)
+def test_gate_up_in_each_form(gpu, T, d, f, E, k, NL, form, _, dyn):
+    D, b, off, g = _routed(T, d, f, E, k, NL, dyn)
+    R = off[-1]
+    xq, xs = _codes(g, T, d), _scales(g, T)
+    w = [(_codes(g, NL * f, d).view(NL, f, d), _scales(g, NL, f)) for _ in range(2)]
+    gu = torch.full((D.R_cap, 2 * f), float(SENTINEL), dtype=BF, device=gpu)
+    h = torch.full((D.R_cap, f), float(SENTINEL), dtype=BF, device=gpu)
+
+    def call(gu):
+        moe.expert_gate_up_i8(D, b.offsets, b.row_token, xq, xs, *w[0], *w[1], gu, h)
+
+    assert R > 0 and _form(lambda: call(gu)) == _as_form(form, dyn)
+    call(gu)
+    tok = b.row_token[:R].long()
+    G, U = (_per_expert(off, xq[tok], xs[tok], *v) for v in w)
+    _same(gu[:R], torch.cat([G, U], 1).to(BF))
+    G, U = G.double().cpu().numpy(), U.double().cpu().numpy()
+    H = G / (1 + np.exp(-G)) * U
+    _within(to_host(h[:R]), H, U32 * (13 + 4 * np.abs(G)) * np.abs(H), True)
+    assert (gu[R:] == SENTINEL).all() and (h[R:] == SENTINEL).all()
+    kept = h.clone()
+    h.fill_(SENTINEL)
+    call(None)
+    assert torch.equal(h, kept)
+
+
+@pytest.mark.parametrize("T,d,f,E,k,NL,_,form,dyn", CASES)
+def test_down_in_each_form(gpu, T, d, f, E, k, NL, _, form, dyn):
+    D, b, off, g = _routed(T, d, f, E, k, NL, dyn)
+    R = off[-1]
+    hq, hs = _codes(g, D.R_cap, f), _scales(g, D.R_cap)
+    hs[R:] = float("nan")
+    wq, ws = _codes(g, NL * d, f).view(NL, d, f), _scales(g, NL, d)
+    y = torch.full((D.R_cap, d), float(SENTINEL), dtype=BF, device=gpu)
+    assert R > 0 and _form(lambda: moe.expert_down_i8(D, b.offsets, hq, hs, wq, ws, y)) == _as_form(form, dyn)
+    moe.expert_down_i8(D, b.offsets, hq, hs, wq, ws, y)
+    _same(y[:R], _per_expert(off, hq, hs, wq, ws).to(BF))
+    assert (y[R:] == SENTINEL).all()
