@@ -15,9 +15,10 @@ import pytest
 import torch
 
 import mixture_experts_layer_02_amd as moe
+import oracle
 from gpu_util import to_host
 from launched import kernels
-from test_gpu_i8 import SENTINEL, U32, _within
+from test_gpu_i8 import SENTINEL, U32, _special_rows, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -208,3 +209,25 @@ def test_down_in_each_form(gpu, T, d, f, E, k, NL, _, form, dyn):
     moe.expert_down_i8(D, b.offsets, hq, hs, wq, ws, y)
     _same(y[:R], _per_expert(off, hq, hs, wq, ws).to(BF))
     assert (y[R:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("rows", [24, 1032])
+@pytest.mark.parametrize("dtype,cols,ldw,ldq", [("bf16", 1, 8, 16), ("bf16", 7, 8, 16), ("bf16", 63, 72, 64), ("bf16", 257, 264, 288),
+                                                ("bf16", 1000, 1000, 1008), ("bf16", 1791, 1792, 1792), ("bf16", 2047, 2048, 2064),
+                                                ("f32", 1, 4, 16), ("f32", 7, 8, 16), ("f32", 63, 72, 64), ("f32", 257, 260, 288),
+                                                ("f32", 1000, 1000, 1008), ("f32", 1023, 1024, 1040)])
+def test_quantiser_of_difficult_rows_in_both_vector_forms(gpu, dtype, cols, ldw, ldq, rows):
+    """Ties, subnormal, huge, zero and non-finite rows with one wave a row (1032 rows) and four (24)."""
+    w = np.concatenate([_special_rows(cols, dtype, 100 * cols + i) for i in range(rows // 24)])
+    src = torch.full((rows, ldw), 1e30, dtype=BF if dtype == "bf16" else F32, device=gpu)
+    src[:, :cols] = torch.from_numpy(w).to(gpu).to(src.dtype)
+    q = torch.full((rows, ldq), SENTINEL, dtype=torch.int8, device=gpu)
+    s = torch.full((rows + 1,), -1.0, device=gpu)
+    (name,) = kernels(lambda: moe.i8_quantize_rows(src[:, :cols], q[:, :cols], s))
+    assert re.search(r"i8_quant_rows_kernelI[tf]Li(\d)ELi(\d+)ELb(\d)E", name).groups() == \
+        (("1", "4", "1") if rows >= 1024 else ("4", "3", "1"))
+    moe.i8_quantize_rows(src[:, :cols], q[:, :cols], s)
+    codes, scale = oracle.i8_quantize_rows(w)
+    np.testing.assert_array_equal(s[:rows].cpu().numpy(), scale)
+    np.testing.assert_array_equal(q[:, :cols].cpu().numpy(), codes)
+    assert (q[:, cols:] == SENTINEL).all() and s[rows] == -1
