@@ -604,7 +604,8 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
   constexpr int KB = NB * MB > 16 ? 1 : 2;             // k-steps whose fragments are read at once
   constexpr bool PIPE = DUAL && WGS == 1;               // (see pipe)
   static_assert(!PIPE || (SW > 2 && NB % 4 == 0), "stages and halves of pipe");
-  static_assert(CW % 2 == 0 && CW * 8 * W == NT && CX * 8 * W == MT && NB % 2 == 0, "shares of the copies; gate and up blocks");
+  static_assert(CW * 8 * W == NT && CX * 8 * W == MT, "shares of the copies");
+  static_assert(!DUAL || (CW % 4 == 0 && NB % 2 == 0), "gate and up blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SW * WST + 2 * XST];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -651,8 +652,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WGS) i8_mid_rows_kernel(I8Params
       for (int j = 0; j < CW; ++j) {
         uint32_t o = vw[j];
         if (decltype(tail_c)::value && i * 128 + piece(row_w(j)) >= p.K) o = 0x80000000u;
-        // (with DUAL bit 4 of an LDS weight row is a bit of j, or of the wave when it copies two times 8 rows)
-        const i32x4 r = DUAL && (CW == 2 ? wave & 1 : j & 2) ? rw2 : rw;
+        const i32x4 r = DUAL && (j & 2) ? rw2 : rw;  // (bit 4 of an LDS weight row: gate or up)
         dma16(r, o, (uint32_t)(i * 128), __builtin_amdgcn_readfirstlane(st + row_w(j) * 128));
       }
     };
