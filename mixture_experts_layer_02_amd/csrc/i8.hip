@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(64 * W, WPS) i8_few_rows_kernel(I8Params p) {
 // rows that the m-tile does not have are left out: the loop is built for each
 // number of them (in steps of a quarter), so that it has no branch and reads all
 // its fragments before it multiplies (with branches and one fragment at a time
-// linear 1000 x 6144 x 1792 took 27 us, now 20), and tokens that are not there
+// linear 1000 x 6144 x 1792 took 27 us, now 21-23), and tokens that are not there
 // are not copied.  Rows are copied half as often per weight as by the kernel
 // above: gate/up of 96 experts, 43 rows each, 387 against 433 us.
 template <int MT, int NT, int WM, int WN, int WGS, int SW, bool DUAL, typename OUT>
@@ -943,8 +943,14 @@ bool use_tiles(int64_t K, int64_t tiles, int64_t mean, bool dual) {
 // and 54; K = 4096, 256 rows, 0.75 65 and 75, 180 rows, 0.53 62 and 52, 128 rows 59
 // and 40) or three (8192 x 4608 x 4096, 0.75: 160 and 177) from three quarters; two
 // want more (K = 6144: 0.75 169 and 158, 0.92 168 and 189; K = 4096, 300 x 49152,
-// 0.44: 116 and 83); a short K three full ones (K = 512, 3 rounds: 54 and 66, one 30
-// and 25).
+// 0.44: 116 and 83); a short K three full ones (8192 x 6144: K = 512 56 and 77, 1024
+// 76 and 100).  One full round of a short K stays off them, although they are
+// ahead there too (4096 x 4096: K = 512 31 and 33, 1024 37 and 42, 1536 43 and 52,
+// 2048, where the limit is, 49 and 60).
+// All without a bias.  With one the tiles are 10 to 57 % slower, the other kernel
+// hardly at all, which the rule does not look at: 16384 x 6144 x 6144 bf16 665-677
+// and 622-628, float32 633-644 and 643-650; 4096^3 97 and 96, 88 and 102; 8192 x
+// 6144 x 2048 180 and 149, 155 and 156; 8192 x 4608 x 4096 245 and 189, 221 and 194.
 bool use_tiles_linear(int64_t M, int64_t N, int64_t K) {
   if (K % 128 || K < 512) return false;
   const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), rounds = cdiv(tiles, num_cus());
