@@ -2,9 +2,10 @@
 
 Argument marshalling only: every step of the layer runs in the library's HIP
 kernels.  PyTorch provides device memory and the current stream.  The
-functions mirror the C ABI in include/moe.h and include/moe_i8.h one to one; ``Buffers``,
-``forward`` and ``backward`` allocate the tensors of one layer pass and chain
-the entry points in order.
+functions mirror the C ABI in include/moe.h, include/moe_i8.h and
+include/moe_decode.h one to one; ``Buffers``, ``forward`` and ``backward``
+allocate the tensors of one layer pass and chain the entry points in order;
+``DecodeBuffers`` and ``decode`` are the same for a few tokens.
 
 There is no fallback: if libmoe.so is missing or fails to load, every call
 raises.
@@ -17,7 +18,7 @@ import os
 import torch  # imported before libmoe.so so that the process holds one HIP runtime
 
 __all__ = [
-    "MoeError", "MoeDesc", "lib", "make_desc", "new_tile_counters", "SCHEDULE_STATIC", "SCHEDULE_DYNAMIC", "workspace_size", "router_logits", "route", "route_grouped", "hold_cus", "fp8_quantize", "fp8_dequantize", "permute", "permute_noalloc", "expert_gate_up_gather", "grouped_ffn_bwd_dw_gather", "expert_gate_up_fp8", "expert_down_fp8", "fp8_quantize_pow2", "expert_gate_up_fp8mm", "fp8_quantize_pow2_rows", "expert_down_fp8mm", "fp8_scale_row_bytes", "i8_quantize_rows", "i8_linear", "expert_gate_up_i8", "expert_down_i8", "Int8Experts", "Int8Buffers", "forward_i8", "row_weights", "dtopk_w_from_parts", "dtopk_parts",
+    "MoeError", "MoeDesc", "lib", "make_desc", "new_tile_counters", "SCHEDULE_STATIC", "SCHEDULE_DYNAMIC", "workspace_size", "router_logits", "route", "route_grouped", "hold_cus", "fp8_quantize", "fp8_dequantize", "permute", "permute_noalloc", "expert_gate_up_gather", "grouped_ffn_bwd_dw_gather", "expert_gate_up_fp8", "expert_down_fp8", "fp8_quantize_pow2", "expert_gate_up_fp8mm", "fp8_quantize_pow2_rows", "expert_down_fp8mm", "fp8_scale_row_bytes", "i8_quantize_rows", "i8_linear", "expert_gate_up_i8", "expert_down_i8", "Int8Experts", "Int8Buffers", "forward_i8", "i4_quantize", "i4_dequantize", "i4_linear", "decode_workspace_size", "DecodeBuffers", "decode", "Int4Experts", "decode_i4", "DECODE_MAX_T", "row_weights", "dtopk_w_from_parts", "dtopk_parts",
     "grouped_ffn", "expert_gate_up", "expert_down", "expert_bwd_dh", "expert_bwd_dx", "expert_bwd_dw_gate_up", "expert_bwd_dw_down", "combine_bwd_gather", "expert_bwd_dh_gather", "expert_bwd_dw_down_gather", "combine", "combine_bwd", "grouped_ffn_bwd_dx", "grouped_ffn_bwd_dw",
     "unpermute_bwd", "unpermute_router_bwd", "route_bwd", "router_bwd", "router_bwd_acc", "Buffers", "forward", "backward",
     "MOE_F32", "MOE_BF16",
@@ -114,6 +115,18 @@ _SIGS_I8 = {
     "moe_expert_down_i8": [_vp, _vp, _vp, _vp, _vp, _vp, _vp],
 }
 EXPORTS_I8 = sorted(list(_SIGS_I8) + ["moe_i8_quantize_rows", "moe_i8_linear"])
+# include/moe_decode.h
+_i, _i64 = ctypes.c_int, ctypes.c_int64
+_SIGS_DECODE = {
+    "moe_i4_quantize": [_vp, _i, _i64, _i64, _i64, _i, _vp, _i64, _vp, _i64, _vp],
+    "moe_i4_dequantize": [_vp, _i64, _vp, _i64, _i64, _i64, _i, _vp, _i, _i64, _vp],
+    "moe_i4_linear": [_i64, _i64, _i64, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i, _vp],
+    "moe_decode_workspace_size": [ctypes.POINTER(MoeDesc), ctypes.POINTER(_sz)],
+    "moe_decode": [ctypes.POINTER(MoeDesc), _i] + [_vp] * 10 + [_sz, _vp],
+    "moe_decode_i4": [ctypes.POINTER(MoeDesc), _i, _i] + [_vp] * 13 + [_sz, _vp],
+}
+EXPORTS_DECODE = sorted(_SIGS_DECODE)
+DECODE_MAX_T = 64
 
 _lib = None
 
@@ -128,6 +141,10 @@ def lib():
         for name, args in {**_SIGS, **_SIGS_I8}.items():
             fn = getattr(l, name)
             fn.argtypes = [ctypes.POINTER(MoeDesc)] + args
+            fn.restype = ctypes.c_int
+        for name, args in _SIGS_DECODE.items():
+            fn = getattr(l, name)
+            fn.argtypes = args
             fn.restype = ctypes.c_int
         l.moe_workspace_size.argtypes = [ctypes.POINTER(MoeDesc), ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
         l.moe_workspace_size.restype = ctypes.c_int
@@ -370,6 +387,60 @@ def expert_down_i8(desc, offsets, hq, hs, w2q, w2s, y_perm):
     _i8("moe_expert_down_i8", dev, ctypes.byref(desc), _flat(offsets, "offsets", NL + 1, torch.int32, dev),
         _flat(hq, "hq", Rc * f, i8, dev), _flat(hs, "hs", Rc, f32, dev), _flat(w2q, "w2q", NL * d * f, i8, dev),
         _flat(w2s, "w2s", NL * d, f32, dev), _flat(y_perm, "y_perm", Rc * d, torch.bfloat16, dev))
+
+
+def _group(group):
+    if group not in (32, 64, 128):
+        raise ValueError(f"group: 32, 64 or 128 values share a scale, not {group}")
+
+
+def _i4_rows(w, q, scale, group, dev):
+    """Arguments of rows of w [rows][cols] beside their 4-bit codes and scales."""
+    _group(group)
+    bf = w.dtype is torch.bfloat16
+    wp, ldw = _rows(w, "w", torch.bfloat16 if bf else torch.float32, dev)
+    qp, ldq = _rows(q, "q", torch.uint8, dev)
+    sp, lds = _rows(scale, "scale", torch.float32, dev)
+    rows, cols = w.shape
+    if q.shape != (rows, cols // 2) or scale.shape != (rows, -(-cols // group)):
+        raise ValueError("w [rows][cols], q [rows][cols / 2] and scale [rows][ceil(cols / group)] do not fit")
+    return wp, MOE_BF16 if bf else MOE_F32, rows, cols, ldw, qp, ldq, sp, lds
+
+
+def i4_quantize(w, q, scale, group=128):
+    """4-bit codes q [rows][cols / 2] (uint8) and scales [rows][ceil(cols / group)]
+    of w [rows][cols] (bf16 or fp32): per group of a row code = 7 w / max (ties to
+    even), scale = max / 7.  Rows may lie apart (q's by a multiple of 4 bytes)."""
+    dev = _device(w, "w")
+    wp, dt, rows, cols, ldw, qp, ldq, sp, lds = _i4_rows(w, q, scale, group, dev)
+    if rows:
+        _i8("moe_i4_quantize", dev, wp, dt, rows, cols, ldw, group, qp, ldq, sp, lds)
+
+
+def i4_dequantize(q, scale, w, group=128):
+    """w [rows][cols] (bf16 or fp32) = scale * code: the values that 4-bit codes stand for."""
+    dev = _device(w, "w")
+    wp, dt, rows, cols, ldw, qp, ldq, sp, lds = _i4_rows(w, q, scale, group, dev)
+    if rows:
+        _i8("moe_i4_dequantize", dev, qp, ldq, sp, lds, rows, cols, group, wp, dt, ldw)
+
+
+def i4_linear(x, wq, ws, y, bias=None, group=128):
+    """y [M][N] (bf16 or fp32) = x [M][K] (bf16) W^T + bias for W in 4 bits: codes
+    wq [N][K / 2] (rows apart by multiples of 16 bytes), scales ws [N][ceil(K / group)]."""
+    _group(group)
+    dev = _device(y, "y")
+    bf = y.dtype is torch.bfloat16
+    xp, ldx = _rows(x, "x", torch.bfloat16, dev)
+    wp, ldw = _rows(wq, "wq", torch.uint8, dev)
+    sp, lds = _rows(ws, "ws", torch.float32, dev)
+    yp, ldy = _rows(y, "y", torch.bfloat16 if bf else torch.float32, dev)
+    (M, K), N = x.shape, wq.shape[0]
+    if wq.shape[1] * 2 != K or ws.shape != (N, -(-K // group)) or y.shape != (M, N):
+        raise ValueError("x [M][K], wq [N][K / 2], ws [N][ceil(K / group)] and y [M][N] do not fit")
+    if M:
+        _i8("moe_i4_linear", dev, M, N, K, group, xp, ldx, wp, ldw, sp, lds,
+            None if bias is None else _flat(bias, "bias", N, torch.float32, dev), yp, ldy, MOE_BF16 if bf else MOE_F32)
 
 
 def fp8_dequantize(q, scales, w):
@@ -644,6 +715,94 @@ def forward_i8(b: Buffers, i8: Int8Buffers, x, wr, experts: Int8Experts, bias=No
     expert_down_i8(D, b.offsets, i8.hq, i8.hs, experts.w2q, experts.w2s, b.y_perm)
     combine(D, b.slot_row, w, b.y_perm, b.y)
     return b.y
+
+
+def decode_workspace_size(desc: MoeDesc) -> int:
+    """Bytes of workspace of decode and decode_i4."""
+    n = ctypes.c_size_t(0)
+    rc = lib().moe_decode_workspace_size(ctypes.byref(desc), ctypes.byref(n))
+    if rc != MOE_OK:
+        raise MoeError("moe_decode_workspace_size", rc)
+    return n.value
+
+
+class DecodeBuffers:
+    """The tensors of decode and decode_i4: the selection, y and the workspace."""
+
+    def __init__(self, desc: MoeDesc, device="cuda"):
+        self.desc = desc
+        self.topk_idx = torch.empty(desc.T, desc.k, dtype=torch.int32, device=device)
+        self.topk_w = torch.empty(desc.T, desc.k, dtype=torch.float32, device=device)
+        self.y = torch.empty(desc.T, desc.d, dtype=torch.bfloat16, device=device)
+        self.ws = torch.empty(decode_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def _decode(name, b, x, wr, weights, bias, routing, n_groups, *group):
+    D, f32, i32, bf = b.desc, torch.float32, torch.int32, torch.bfloat16
+    T, d, E, k = D.T, D.d, D.E, D.k
+    dev = _device(b.y, "y")
+    if routing is None:
+        idx, w = b.topk_idx, b.topk_w
+        wrp = _flat(wr, "wr", E * d, bf, dev)
+        bp = None if bias is None else _flat(bias, "bias", E, f32, dev)
+    else:
+        (idx, w), wrp, bp, n_groups = routing, None, None, 1
+    _i8(name, dev, ctypes.byref(D), *group, int(n_groups), _flat(x, "x", T * d, bf, dev), wrp, bp, *weights(dev),
+        _flat(idx, "topk_idx", T * k, i32, dev), _flat(w, "topk_w", T * k, f32, dev), _flat(b.y, "y", T * d, bf, dev),
+        _flat(b.ws, "ws", 1, torch.uint8, dev), b.ws.numel())
+    return b.y
+
+
+def decode(b: DecodeBuffers, x, wr, w1, w3, w2, bias=None, routing=None, n_groups=1):
+    """forward for up to DECODE_MAX_T tokens in one call (bf16): the router, the
+    experts and the combine -> b.y, with the selection in b.topk_idx and b.topk_w.
+    ``routing=(topk_idx, topk_w)`` device tensors skip the router (wr is not read)."""
+    D = b.desc
+    n = D.num_local * D.f * D.d
+
+    def weights(dev):
+        return [_flat(t, name, n, torch.bfloat16, dev) for name, t in (("w1", w1), ("w3", w3), ("w2", w2))]
+
+    return _decode("moe_decode", b, x, wr, weights, bias, routing, n_groups)
+
+
+class Int4Experts:
+    """The experts' weights in 4 bits with one scale per group of a row, made once
+    from W1, W3 [NL][f][d] and W2 [NL][d][f]."""
+
+    def __init__(self, w1, w3, w2, group=128):
+        self.group = group
+        for name, w in (("w1", w1), ("w3", w3), ("w2", w2)):
+            n, rows, cols = w.shape
+            q = torch.empty(n, rows, cols // 2, dtype=torch.uint8, device=w.device)
+            s = torch.empty(n, rows, -(-cols // group), dtype=torch.float32, device=w.device)
+            i4_quantize(w.view(n * rows, cols), q.view(n * rows, cols // 2), s.view(n * rows, -1), group)
+            setattr(self, name + "q", q)
+            setattr(self, name + "s", s)
+
+    @classmethod
+    def from_codes(cls, w1q, w1s, w3q, w3s, w2q, w2s, group=128):
+        """From codes and scales that are there already (as i4_quantize writes them)."""
+        e = cls.__new__(cls)
+        e.group, e.w1q, e.w1s, e.w3q, e.w3s, e.w2q, e.w2s = group, w1q, w1s, w3q, w3s, w2q, w2s
+        return e
+
+
+def decode_i4(b: DecodeBuffers, x, wr, experts: Int4Experts, bias=None, routing=None, n_groups=1):
+    """decode with the experts' weights in 4 bits."""
+    D, g = b.desc, experts.group
+    NL, d, f = D.num_local, D.d, D.f
+    _group(g)
+    nd, nf = NL * f * -(-d // g), NL * d * -(-f // g)
+
+    def weights(dev):
+        out = []
+        for name, ns in (("w1", nd), ("w3", nd), ("w2", nf)):
+            out.append(_flat(getattr(experts, name + "q"), name + "q", NL * f * d // 2, torch.uint8, dev))
+            out.append(_flat(getattr(experts, name + "s"), name + "s", ns, torch.float32, dev))
+        return out
+
+    return _decode("moe_decode_i4", b, x, wr, weights, bias, routing, n_groups, g)
 
 
 def backward(b: Buffers, x, wr, w1, w3, w2, dy, routing=None, fuse_router_dx=True):

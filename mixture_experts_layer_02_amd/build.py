@@ -22,7 +22,7 @@ ARCH = "gfx950"
 # packed-fp32-ops off: the v_pk_*_f32 forms are not trusted on these parts.
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "hold.hip", "fp8.hip", "i8.hip"]
+SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "hold.hip", "fp8.hip", "i8.hip", "i4.hip", "decode.hip"]
 # ffn.hip: the GEMMs' dynamic tile claims are one lane's atomic whose result is
 # used a k-tile later; LLVM's atomic optimizer would rewrite them into a form
 # that waits for the result at once (and for every load in flight before it).

@@ -487,6 +487,98 @@ int moe_expert_down_i8(const moe_desc* desc, const int32_t* offsets, const int8_
   return finish(moe::launch_down_i8(*desc, offsets, hq, hs, W2q, W2s, y_perm, S(stream)));
 }
 
+// Rows of codes, scales and activations are addressed with 32-bit offsets
+// within a tile.
+constexpr int64_t I4_MAX_K = 1 << 20, I4_MAX_LD = 1 << 21;
+static bool i4_group(int group) { return group == 32 || group == 64 || group == 128; }
+static bool need4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Rows of 4-bit codes and their scales beside rows of w.
+static int i4_rows(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw, int group, const uint8_t* q,
+                   int64_t ldq, const float* scale, int64_t lds) {
+  if (!need(w) || !need(q) || !need4(scale) || rows < 0 || cols < 8 || cols % 8 || ldw < cols || ldq < cols / 2 || ldq % 4)
+    return MOE_ERR_INVALID_ARG;
+  if (!i4_group(group) || (dtype != MOE_BF16 && dtype != MOE_F32) || cols > 1 << 28) return MOE_ERR_UNSUPPORTED;
+  return lds < (cols + group - 1) / group ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+int moe_i4_quantize(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw, int group, uint8_t* q,
+                    int64_t ldq, float* scale, int64_t lds, void* stream) {
+  int rc = i4_rows(w, dtype, rows, cols, ldw, group, q, ldq, scale, lds);
+  if (rc) return rc;
+  return finish(moe::launch_i4_quantize(w, dtype, rows, cols, ldw, group, q, ldq, scale, lds, S(stream)));
+}
+
+int moe_i4_dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t lds, int64_t rows, int64_t cols,
+                      int group, void* w, int dtype, int64_t ldw, void* stream) {
+  int rc = i4_rows(w, dtype, rows, cols, ldw, group, q, ldq, scale, lds);
+  if (rc) return rc;
+  return finish(moe::launch_i4_dequantize(q, ldq, scale, lds, rows, cols, group, w, dtype, ldw, S(stream)));
+}
+
+int moe_i4_linear(int64_t M, int64_t N, int64_t K, int group, const void* x, int64_t ldx, const uint8_t* wq,
+                  int64_t ldw, const float* ws, int64_t lds, const float* bias, void* y, int64_t ldy, int dtype,
+                  void* stream) {
+  if (!need(x) || !need(wq) || !need4(ws) || !opt(bias) || !need(y) || M < 0 || N < 1 || K < 8 || K % 8 || ldx < K ||
+      ldx % 8 || ldw < K / 2 || ldw % 16 || ldy < N)
+    return MOE_ERR_INVALID_ARG;
+  if (!i4_group(group) || (dtype != MOE_BF16 && dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
+  if (lds < (K + group - 1) / group) return MOE_ERR_INVALID_ARG;
+  if (K > I4_MAX_K || ldx > I4_MAX_LD || ldw > I4_MAX_LD || lds > I4_MAX_LD || M >= (1ll << 31) - 256 ||
+      N >= (1ll << 31) - 256)
+    return MOE_ERR_UNSUPPORTED;
+  return finish(moe::launch_i4_linear(M, N, K, group, x, ldx, wq, ldw, ws, lds, bias, y, ldy, dtype, S(stream)));
+}
+
+static int check_decode(const moe_desc* d) {
+  int rc = check_desc(d);
+  if (rc) return rc;
+  return d->T > MOE_DECODE_MAX_T || d->dtype != MOE_BF16 || d->d > 1 << 20 || d->f > 1 << 20 ? MOE_ERR_UNSUPPORTED
+                                                                                              : MOE_OK;
+}
+
+int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes) {
+  int rc = check_decode(desc);
+  if (rc) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = moe::decode_workspace(*desc);
+  return MOE_OK;
+}
+
+// What moe_decode and moe_decode_i4 have in common.
+static int decode(const moe_desc* desc, int group, int n_groups, const void* x, const void* Wr, const float* bias,
+                  const void* W1, const float* W1s, const void* W3, const float* W3s, const void* W2, const float* W2s,
+                  int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!need(x) || !opt(Wr) || !opt(bias) || !need(W1) || !need(W3) || !need(W2) || !need(topk_idx) || !need(topk_w) ||
+      !need(y))
+    return MOE_ERR_INVALID_ARG;
+  if (n_groups < 1 || n_groups > 64 || desc->E % n_groups || desc->k % n_groups) return MOE_ERR_INVALID_ARG;
+  if (!Wr && (bias || n_groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (!need(ws) || ws_bytes < moe::decode_workspace(*desc)) return ws ? MOE_ERR_WORKSPACE : MOE_ERR_INVALID_ARG;
+  return finish(moe::launch_decode(*desc, group, n_groups, x, Wr, bias, W1, W1s, W3, W3s, W2, W2s, topk_idx, topk_w, y,
+                                   ws, S(stream)));
+}
+
+int moe_decode(const moe_desc* desc, int n_groups, const void* x, const void* Wr, const float* bias, const void* W1,
+               const void* W3, const void* W2, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
+               void* stream) {
+  int rc = check_decode(desc);
+  if (rc) return rc;
+  return decode(desc, 0, n_groups, x, Wr, bias, W1, nullptr, W3, nullptr, W2, nullptr, topk_idx, topk_w, y, ws, ws_bytes,
+                stream);
+}
+
+int moe_decode_i4(const moe_desc* desc, int group, int n_groups, const void* x, const void* Wr, const float* bias,
+                  const uint8_t* W1q, const float* W1s, const uint8_t* W3q, const float* W3s, const uint8_t* W2q,
+                  const float* W2s, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_decode(desc);
+  if (rc) return rc;
+  if (!i4_group(group)) return MOE_ERR_UNSUPPORTED;
+  if (!need(W1s) || !need(W3s) || !need(W2s)) return MOE_ERR_INVALID_ARG;
+  return decode(desc, group, n_groups, x, Wr, bias, W1q, W1s, W3q, W3s, W2q, W2s, topk_idx, topk_w, y, ws, ws_bytes,
+                stream);
+}
+
 int moe_hold_cus(int workgroups, int lds_bytes, int microseconds, void* stream) {
   if (workgroups < 1 || workgroups > 4096 || lds_bytes < 4 || lds_bytes > 160 * 1024 || microseconds < 0 ||
       microseconds > 1000000)

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moe_decode.h"
 #include "../../include/moe_i8.h"
 
 namespace moe {

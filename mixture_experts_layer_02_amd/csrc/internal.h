@@ -44,6 +44,19 @@ hipError_t launch_i8_linear(int64_t M, int64_t N, int64_t K, const int8_t* xq, i
                             const int8_t* wq, int64_t ldw, const float* ws, const float* bias, void* y, int64_t ldy,
                             int dtype, hipStream_t s);
 
+hipError_t launch_i4_quantize(const void* w, int dtype, int64_t rows, int64_t cols, int64_t ldw, int group, uint8_t* q,
+                              int64_t ldq, float* scale, int64_t lds, hipStream_t s);
+hipError_t launch_i4_dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t lds, int64_t rows,
+                                int64_t cols, int group, void* w, int dtype, int64_t ldw, hipStream_t s);
+hipError_t launch_i4_linear(int64_t M, int64_t N, int64_t K, int group, const void* x, int64_t ldx, const uint8_t* wq,
+                            int64_t ldw, const float* ws, int64_t lds, const float* bias, void* y, int64_t ldy,
+                            int dtype, hipStream_t s);
+// group 0: bf16 weights (no scales); Wr NULL: idx and w are read.
+size_t decode_workspace(const moe_desc& d);
+hipError_t launch_decode(const moe_desc& d, int group, int n_groups, const void* x, const void* Wr, const float* bias,
+                         const void* W1, const float* W1s, const void* W3, const float* W3s, const void* W2,
+                         const float* W2s, int32_t* idx, float* w, void* y, void* ws, hipStream_t s);
+
 size_t permute_workspace(const moe_desc& d);
 // Size of the allocation-free permute's fixed device scratch (4 MiB per device).
 constexpr size_t PERMUTE_SCRATCH_BYTES = (size_t)4 << 20;

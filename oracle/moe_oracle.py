@@ -50,6 +50,7 @@ __all__ = [
     "combine_bwd", "expert_ffn_bwd_rows", "expert_ffn_bwd", "unpermute_bwd",
     "route_bwd", "router_bwd", "layer_forward", "layer_backward",
     "i8_quantize_rows", "i8_dequantize_rows", "i8_linear",
+    "i4_quantize", "i4_pack", "i4_unpack", "i4_dequantize", "i4_linear",
 ]
 
 
@@ -634,4 +635,63 @@ def i8_dequantize_rows(codes, scale):
 def i8_linear(xq, xs, wq, ws, bias=None):
     """y [M][N] = xs ws (xq wq^T) + bias: the product of whole numbers is exact in float64."""
     y = (_f64(xq) @ _f64(wq).T) * _f64(xs)[:, None] * _f64(ws)[None, :]
+    return y if bias is None else y + _f64(bias)[None, :]
+
+
+# --------------------------------------------------------------------------
+# 4-bit codes with one scale per group of a row.
+# --------------------------------------------------------------------------
+def i4_pack(codes):
+    """Bytes [rows][cols / 2] of codes [rows][cols] in [-8, 7]: eight codes share a
+    32-bit word (low byte first), code i plus 8 at bit 4 (i / 2 + 4 (i % 2))."""
+    c = np.asarray(codes, np.int64) + 8
+    assert c.shape[1] % 8 == 0 and c.min(initial=0) >= 0 and c.max(initial=0) <= 15
+    word = np.zeros((c.shape[0], c.shape[1] // 8), np.int64)
+    for i in range(8):
+        word |= c[:, i::8] << (4 * (i // 2 + 4 * (i % 2)))
+    return np.ascontiguousarray(word.astype("<u4")).view(np.uint8)
+
+
+def i4_unpack(q):
+    """Codes [rows][cols] (int8) of bytes [rows][cols / 2]."""
+    word = np.ascontiguousarray(q).view("<u4").astype(np.int64)
+    out = np.empty((word.shape[0], word.shape[1] * 8), np.int8)
+    for i in range(8):
+        out[:, i::8] = (word >> (4 * (i // 2 + 4 * (i % 2))) & 15) - 8
+    return out
+
+
+def i4_quantize(w, group):
+    """codes [rows][cols] int8 and scales [rows][ceil(cols / group)] float32 of w.
+
+    Per group of a row with m = max |w|: scale = m / 7 (float32), code = 7 w / m to
+    the nearest integer, ties to even (in float64, which decides as the exact
+    quotient does: 14 w and (2n + 1) m are whole numbers below 2^28 times a
+    power of two).  A group of zeros has scale 0; one that is not finite has
+    scale NaN; both have codes 0.
+    """
+    w = np.asarray(w, np.float32)
+    rows, cols = w.shape
+    codes = np.empty((rows, cols), np.int8)
+    scale = np.empty((rows, -(-cols // group)), np.float32)
+    for j, lo in enumerate(range(0, cols, group)):
+        v = w[:, lo:lo + group]
+        m = np.abs(v).max(axis=1).astype(np.float64)
+        live = np.isfinite(m) & (m > 0)
+        with np.errstate(invalid="ignore"):
+            q = np.rint(v.astype(np.float64) * 7.0 / np.where(live, m, 1.0)[:, None])
+            scale[:, j] = np.where(np.isfinite(m), m.astype(np.float32) / np.float32(7), np.float32(np.nan))
+        codes[:, lo:lo + group] = np.where(live[:, None], q, 0.0).astype(np.int8)
+    return codes, scale
+
+
+def i4_dequantize(codes, scale, group):
+    """The float64 values the codes stand for."""
+    codes = np.asarray(codes, np.float64)
+    return codes * np.repeat(np.asarray(scale, np.float64), group, axis=1)[:, :codes.shape[1]]
+
+
+def i4_linear(x, codes, scale, group, bias=None):
+    """y [M][N] = x W^T + bias for W [N][K] in codes and scales."""
+    y = _f64(x) @ i4_dequantize(codes, scale, group).T
     return y if bias is None else y + _f64(bias)[None, :]
