@@ -39,7 +39,7 @@ def _run(cmd):
 
 # Sources holding the LDS-DMA GEMM kernels: their device assembly is checked
 # for the SGPR wait-state hazard of the inline-asm DMA (hazard_check.py).
-CHECKED = ["ffn.hip", "fp8.hip", "i8.hip"]
+CHECKED = ["ffn.hip", "fp8.hip", "i8.hip", "i4.hip", "decode.hip"]
 
 
 def _compile(light: bool, verbose: bool):

@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "stream.h"
 
 namespace moe {
 
@@ -156,35 +157,117 @@ hipError_t dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t
   return hipGetLastError();
 }
 
-// One wave per output: each lane takes every 64th word of the channel's row.
-template <int GRP, typename OUT>
-__global__ void __launch_bounds__(256) i4_linear_kernel(int64_t M, int64_t N, int64_t words, const uint16_t* __restrict__ x,
-                                                        int64_t ldx, const uint8_t* __restrict__ wq, int64_t ldw,
-                                                        const float* __restrict__ ws, int64_t lds,
-                                                        const float* __restrict__ bias, OUT* __restrict__ y, int64_t ldy) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < M * N; i += (int64_t)gridDim.x * 4) {
-    const int64_t m = i / N, n = i % N;
-    float sum = 0.f;
-    for (int64_t word = lane; word < words; word += 64) {
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(wq + n * ldw + word * 4);
-      float v[8], part = 0.f;
-      Vec16<uint16_t>::load(x + m * ldx + word * 8, v);
+// The linear layer: a workgroup computes RB rows x R channels over all of K, whose
+// stretches of 256 its W waves take in turn, each through a ring of S stages
+// (stream.h).
+struct LinearParams {
+  const uint16_t* x;
+  const uint8_t* w;
+  const float* s;
+  const float* bias;
+  void* y;
+  int64_t ldx, ldw, lds, ldy;
+  int M, N, K;
+  int mblocks, ntiles;
+  int64_t items;
+};
+
+template <int GRP, int RB, int R, int W, int S, typename OUT>
+__global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
+  using namespace stream;
+  using ST = Stage<GRP, R, 1, false, RB>;
+  constexpr int RED = W * RB * (R + 4) * 4;
+  constexpr int RING = W * S * ST::BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > RED ? RING : RED];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Blocks of rows that share channels run side by side on one XCD (workgroups
+  // go to the eight in turn), whose L2 serves the weights to all but the first.
+  for (int64_t id = blockIdx.x; id < p.items; id += gridDim.x) {
+  const int mb = (int)((id >> 3) % p.mblocks);
+  const int64_t tile = (id >> 3) / p.mblocks * 8 + (id & 7);
+  if (tile >= p.ntiles) continue;
+  const int m0 = mb * RB, rows = min(RB, p.M - m0), n0 = (int)tile * R, chans = min(R, p.N - n0);
+
+  Source src;
+  src.w[0] = src.w[1] = make_rsrc(p.w + n0 * p.ldw, (uint64_t)(chans - 1) * p.ldw + p.K / 2);
+  src.s[0] = src.s[1] = make_rsrc(p.s + n0 * p.lds, (uint64_t)chans * p.lds * 4);
+  src.x = make_rsrc(p.x + m0 * p.ldx, (uint64_t)rows * p.ldx * 2);
+  src.pitch = (uint32_t)p.ldw;
+  src.spitch = (uint32_t)p.lds * 4;
+  src.K = p.K;
+  src.rows = chans;
+  uint32_t xr[ST::XI];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part += v[j] * (float)((int)((c >> (4 * ((j >> 1) + 4 * (j & 1)))) & 15u) - 8);
-      sum += ws[n * lds + word / (GRP / 8)] * part;
-    }
-    sum = wave_sum(sum);
-    if (lane == 0) Elem<OUT>::st(y + m * ldy, n, sum + (bias ? bias[n] : 0.f));
+  for (int n = 0; n < ST::XI; ++n) {
+    const int row = ST::x_row(n, lane);
+    xr[n] = row < rows ? (uint32_t)(row * p.ldx * 2) : NOWHERE;
+  }
+  const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * S * ST::BYTES;
+  const uint8_t* ring_p = smem + wave * S * ST::BYTES;
+  const int chunks = (p.K + 255) / 256;
+  const int mine = (chunks - wave + W - 1) / W;  // stretches wave, wave + W, ...
+  auto copy = [&](int i, int slot) {
+    const int k0 = __builtin_amdgcn_readfirstlane((wave + W * i) * 256);
+    const uint32_t at = __builtin_amdgcn_readfirstlane(ring + slot * ST::BYTES);
+    ST::copy_w(src, k0, at, lane);
+    ST::copy_x(src, xr, k0, at, lane);
+  };
+  f32x4_t acc[ST::RT];
+#pragma unroll
+  for (int t = 0; t < ST::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    if (i < mine) copy(i, i);
+  int slot = 0;
+  for (int i = 0; i < mine; ++i) {
+    if (i + S <= mine) wait_vm<(S - 1) * (ST::WI + ST::SI + ST::XI)>();
+    else wait_vm<0>();
+    asm volatile("" ::: "memory");
+    ST st;
+    st.read(ring_p + slot * ST::BYTES, lane);
+    reads_done();
+    if (i + S < mine) copy(i + S, slot);
+    st.multiply(acc);
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  // Partial sums [wave][row][channel] over the ring, once every wave is done with it.
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);
+  const int col = lane & 15;
+  if (col < RB && (R > 8 || lane < 32)) {
+#pragma unroll
+    for (int t = 0; t < ST::RT; ++t)
+      *reinterpret_cast<f32x4_t*>(red + (wave * RB + col) * (R + 4) + 16 * t + 4 * (lane >> 4)) = acc[t];
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * R; i += 64 * W) {
+    const int row = i / R, c = i % R;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += red[(w * RB + row) * (R + 4) + c];
+    if (c < chans) Elem<OUT>::st((OUT*)p.y + (m0 + row) * p.ldy, n0 + c, p.bias ? sum + p.bias[n0 + c] : sum);
+  }
+  __syncthreads();  // the next tile's copies overwrite the partial sums
   }
 }
 
-template <int GRP, typename OUT>
-hipError_t linear(int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const uint8_t* wq, int64_t ldw,
-                  const float* ws, int64_t lds, const float* bias, void* y, int64_t ldy, hipStream_t s) {
-  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(M * N, 4), (int64_t)num_cus() * 64);
-  i4_linear_kernel<GRP, OUT><<<grid, 256, 0, s>>>(M, N, K / 8, (const uint16_t*)x, ldx, wq, ldw, ws, lds, bias, (OUT*)y, ldy);
+template <int GRP, int RB, int R, int W, int S, typename OUT>
+hipError_t run_linear(LinearParams p, hipStream_t s) {
+  p.mblocks = (int)cdiv(p.M, RB);
+  p.ntiles = (int)cdiv(p.N, R);
+  p.items = cdiv(p.ntiles, 8) * 8 * p.mblocks;
+  const unsigned grid = (unsigned)std::min<int64_t>(p.items, 1 << 22);
+  i4_linear_kernel<GRP, RB, R, W, S, OUT><<<grid, 64 * W, 0, s>>>(p);
   return hipGetLastError();
+}
+
+template <int GRP, typename OUT>
+hipError_t linear(const LinearParams& p, hipStream_t s) {
+  if (p.M == 1) return run_linear<GRP, 1, 16, 8, 2, OUT>(p, s);
+  if (p.M <= 4) return run_linear<GRP, 4, 16, 8, 2, OUT>(p, s);
+  if (p.M <= 16) return run_linear<GRP, 16, 32, 4, 2, OUT>(p, s);
+  return run_linear<GRP, 16, 64, 4, 2, OUT>(p, s);
 }
 
 }  // namespace
@@ -215,11 +298,10 @@ hipError_t launch_i4_linear(int64_t M, int64_t N, int64_t K, int group, const vo
                             int64_t ldw, const float* ws, int64_t lds, const float* bias, void* y, int64_t ldy,
                             int dtype, hipStream_t s) {
   if (M == 0) return hipSuccess;
+  const LinearParams p{(const uint16_t*)x, wq, ws, bias, y, ldx, ldw, lds, ldy, (int)M, (int)N, (int)K, 0, 0, 0};
   auto run = [&](auto o) {
     using OUT = decltype(o);
-    return group == 32   ? linear<32, OUT>(M, N, K, x, ldx, wq, ldw, ws, lds, bias, y, ldy, s)
-           : group == 64 ? linear<64, OUT>(M, N, K, x, ldx, wq, ldw, ws, lds, bias, y, ldy, s)
-                         : linear<128, OUT>(M, N, K, x, ldx, wq, ldw, ws, lds, bias, y, ldy, s);
+    return group == 32 ? linear<32, OUT>(p, s) : group == 64 ? linear<64, OUT>(p, s) : linear<128, OUT>(p, s);
   };
   return dtype == MOE_F32 ? run(0.f) : run((uint16_t)0);
 }

@@ -1,0 +1,221 @@
+// Weights streamed through LDS to the matrix cores, for products of few rows:
+// the pieces that the 4-bit linear layer and the decode step share.
+//
+// Such a product reads each weight once and is bound by HBM, so a wave keeps
+// many loads in flight: it owns a ring of stages in LDS that it fills by LDS
+// DMA, a stage holding the same stretch of k of R weight rows (channels) and of
+// RB activation rows (tokens), and takes them in order, with no barrier: waves
+// of a workgroup split k between them and add their sums at the end.
+//
+// Fragments are those of v_mfma_f32_16x16x32_bf16 with the channels as rows and
+// the tokens as columns: lane l holds eight values of row l % 16 at k = 8 (l / 16),
+// and of the result rows 4 (l / 16) .. + 3 of column l % 16.
+//
+// 4-bit codes q enter as the bf16 values 24 + q: a nibble n = q + 8 set into the
+// upper four mantissa bits of 16 gives 16 + n, so that a word of eight codes becomes
+// four registers by a shift and an and-or each.  The 24 times the sum of x that
+// comes with it is taken off by products with a constant -24, whose sum the
+// accumulator starts from.  All of it is exact but for the float32 sums, whose
+// terms are up to 56 |x| in place of 8 |x|: 3 bits of 24.
+#pragma once
+
+#include "gemm_dma.h"
+
+namespace moe {
+namespace stream {
+
+using dma::dma16;
+using dma::i32x4;
+using dma::make_rsrc;
+using dma::touch4u;
+using dma::wait_vm;
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t NOWHERE = 0x80000000u;  // an offset past every resource: the copy writes zeros
+
+// What a stage's copies read: the weights' rows (DUAL: of two matrices), their
+// scales, the activations.  Bases may differ from tile to tile, pitches are in bytes.
+struct Source {
+  i32x4 w[2], s[2], x;
+  uint32_t pitch, spitch;  // of a row of weights; of a row of scales
+  int K, rows;             // k in all; rows of a part that exist
+};
+
+// GRP 0: bf16 weights; else 4 bits with a scale per GRP.  R weight rows (8, or a
+// multiple of 16; DUAL: eight of the first matrix, eight of the second, and so
+// on) by SUB pieces of 128 bytes, RB activation rows.
+template <int GRP, int R, int SUB, bool DUAL, int RB>
+struct Stage {
+  static constexpr bool I4 = GRP > 0;
+  static constexpr int KC = I4 ? 256 : 64, KS = KC * SUB;  // k of a piece; of a stage
+  static constexpr int PARTS = DUAL ? 2 : 1, PR = R / PARTS, RT = (R + 15) / 16;
+  static constexpr int WB = R * SUB * 128, WI = WB / 1024;               // bytes; copies
+  static constexpr int GPC = I4 ? KC / (I4 ? GRP : 1) : 0;               // groups of a stage
+  static constexpr int SIP = (GPC * PR + 63) / 64, SI = SIP * PARTS, SB = SI * 256;
+  static constexpr int XROW = KC * 2, XB = SUB * RB * XROW, XI = (XB + 1023) / 1024;
+  static constexpr int BYTES = WB + SB + XB;
+  static constexpr int STEPS = SUB * KC / 32;  // products of 32 k
+  static_assert(!I4 || SUB == 1, "one piece of a 4-bit row per stage");
+  static_assert(R == 8 || R % 16 == 0, "rows");
+  static_assert((GPC & (GPC - 1)) == 0 && (PR & (PR - 1)) == 0, "powers of two");
+
+  // LDS rows of weights are 128 bytes, 16-byte piece c of row r at c ^ (r & 6): the
+  // 16 lanes that a ds_read_b128 serves at once then read from all banks.  The
+  // activations' rows of 32 pieces (4 bits) keep piece 4 a + b of a half at
+  // (4 b + a) ^ r for the same reason.
+  static __device__ __forceinline__ int x_piece(int pos, int row) {
+    if (!I4) return pos ^ (row & 6);
+    const int p = (pos & 15) ^ (row & 15);
+    return (pos & 16) | ((p & 3) << 2) | (p >> 2);
+  }
+  static __device__ __forceinline__ int x_pos(int piece, int row) {
+    if (!I4) return piece ^ (row & 6);
+    const int p = piece & 15;
+    return (piece & 16) | ((((p & 3) << 2) | (p >> 2)) ^ (row & 15));
+  }
+
+  // Row of the activations that lane l's part of copy n belongs to.
+  static __device__ __forceinline__ int x_row(int n, int lane) { return ((n * 1024 + lane * 16) / XROW) % RB; }
+
+  // Copies of the stage at k0 into LDS at `slot`: the weights and their scales.
+  // A piece of a row that lies past K, or a row past `rows`, is not read.
+  static __device__ __forceinline__ void copy_w(const Source& s, int k0, uint32_t slot, int lane) {
+    const int r8 = lane >> 3, piece = (lane & 7) ^ (r8 & 6);
+    const int row_bytes = I4 ? (s.K / 2 + 15) & ~15 : s.K * 2;
+    const int at = I4 ? k0 / 2 : k0 * 2;
+    const bool tail = at + SUB * 128 > row_bytes;  // (uniform)
+#pragma unroll
+    for (int j = 0; j < WI; ++j) {
+      const int sub = j / (R / 8), jr = j % (R / 8);
+      const int part = DUAL ? jr & 1 : 0, row = (DUAL ? jr >> 1 : jr) * 8 + r8;
+      uint32_t v = (uint32_t)row * s.pitch + (uint32_t)(sub * 128 + piece * 16);
+      if (row >= s.rows || (tail && at + sub * 128 + piece * 16 >= row_bytes)) v = NOWHERE;
+      dma16(s.w[part], v, (uint32_t)at, __builtin_amdgcn_readfirstlane(slot + j * 1024));
+    }
+    if constexpr (I4) {
+      const int g0 = k0 / GRP, groups = (s.K + GRP - 1) / GRP;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int n = 0; n < SIP; ++n) {
+          const int i = n * 64 + lane, g = i / PR, row = i % PR;
+          const uint32_t v = g >= GPC || g0 + g >= groups || row >= s.rows
+                                 ? NOWHERE : (uint32_t)row * s.spitch + (uint32_t)g * 4;
+          touch4u(s.s[p], v, (uint32_t)(g0 * 4),
+                  __builtin_amdgcn_readfirstlane(slot + WB + (p * SIP + n) * 256));
+        }
+    }
+  }
+
+  // ... and the activations; xr[n] is the byte offset of row x_row(n, lane), or
+  // NOWHERE.  Zeros past K.
+  static __device__ __forceinline__ void copy_x(const Source& s, const uint32_t (&xr)[XI], int k0, uint32_t slot,
+                                                int lane) {
+#pragma unroll
+    for (int n = 0; n < XI; ++n) {
+      const int byte = n * 1024 + lane * 16;
+      const int k = (byte / (RB * XROW)) * KC + x_piece((byte % XROW) / 16, x_row(n, lane)) * 8;
+      const uint32_t v = k0 + k >= s.K ? NOWHERE : xr[n] + (uint32_t)k * 2;
+      if (XB % 1024 == 0 || byte < XB)
+        dma16(s.x, v, (uint32_t)k0 * 2, __builtin_amdgcn_readfirstlane(slot + WB + SB + n * 1024));
+    }
+  }
+
+  // A stage in registers, and its products added to acc (rows 16 t + 4 (l / 16)
+  // .. + 3, column l % 16; columns from RB on repeat others).
+  bf16x8 b[STEPS];
+  u32x4_t a[I4 ? 1 : STEPS][I4 ? 1 : RT];
+  uint32_t c[I4 ? RT : 1][8];
+  f32x4_t sc[I4 ? GPC : 1][I4 ? RT : 1];
+
+  __device__ __forceinline__ void read(const uint8_t* slot, int lane) {
+    const int r = lane & 15, q = lane >> 4, col = r % RB;
+    auto xb = [&](int sub, int piece) {
+      return *reinterpret_cast<const bf16x8*>(slot + WB + SB + (sub * RB + col) * XROW + x_pos(piece, col) * 16);
+    };
+    if constexpr (!I4) {
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const int sub = st / 2, ks = st % 2;
+        b[st] = xb(sub, 4 * ks + q);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int row = R == 8 ? r & 7 : 16 * t + r;
+          a[st][t] = *reinterpret_cast<const u32x4_t*>(slot + (sub * R + row) * 128 + (((4 * ks + q) ^ (row & 6)) << 4));
+        }
+      }
+    } else {
+      constexpr int NJ = GRP / 32;  // words of a group that a lane holds
+#pragma unroll
+      for (int st = 0; st < 8; ++st) b[st] = xb(0, (st / NJ) * (4 * NJ) + q * NJ + st % NJ);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int row = R == 8 ? r & 7 : 16 * t + r;
+        const uint8_t* w = slot + row * 128;
+        auto at = [&](int word) { return w + (((word >> 2) ^ (row & 6)) << 4) + (word & 3) * 4; };
+#pragma unroll
+        for (int g = 0; g < GPC; ++g) {
+          if constexpr (NJ == 4) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(16 * g + 4 * q));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[t][4 * g + j] = v[j];
+          } else if constexpr (NJ == 2) {
+            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at(8 * g + 2 * q));
+            c[t][2 * g] = v[0], c[t][2 * g + 1] = v[1];
+          } else {
+            c[t][g] = *reinterpret_cast<const uint32_t*>(at(4 * g + q));
+          }
+          const int part = DUAL ? q >> 1 : 0;
+          const int srow = DUAL ? 8 * t + 4 * (q & 1) : R == 8 ? 4 * (q & 1) : 16 * t + 4 * q;
+          sc[g][t] = *reinterpret_cast<const f32x4_t*>(slot + WB + part * SIP * 256 + (g * PR + srow) * 4);
+        }
+      }
+    }
+  }
+
+  static __device__ __forceinline__ bf16x8 codes(uint32_t w) {
+    constexpr uint32_t M = 0x00780078u, O = 0x41804180u;
+    const u32x4_t v = {((w << 3) & M) | O, ((w >> 1) & M) | O, ((w >> 5) & M) | O, ((w >> 9) & M) | O};
+    return __builtin_bit_cast(bf16x8, v);
+  }
+
+  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RT]) const {
+    if constexpr (!I4) {
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[st][t]), b[st], acc[t], 0, 0, 0);
+    } else {
+      constexpr int NJ = GRP / 32;
+      const bf16x8 off = __builtin_bit_cast(bf16x8, u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
+#pragma unroll
+      for (int g = 0; g < GPC; ++g) {
+        f32x4_t base = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) base = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, b[g * NJ + j], base, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          f32x4_t p = base;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes(c[t][g * NJ + j]), b[g * NJ + j], p, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] += sc[g][t][i] * p[i];
+        }
+      }
+    }
+  }
+};
+
+// LDS reads of a stage are complete before its slot is copied over.
+__device__ __forceinline__ void reads_done() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace stream
+}  // namespace moe
