@@ -1,7 +1,7 @@
 /*
  * moe_decode.h -- the entry points of libmoe.so for decoding: weights in 4
  * bits with group scales, a linear layer on them, and the whole expert layer
- * of moe.h (A1 to A7) for a few tokens in one call, with the experts'
+ * of moe.h (A1 to A7) for a few tokens in two kernels, with the experts'
  * weights in bf16 or in 4 bits.  The conventions of moe.h hold: device
  * pointers owned by the caller and 16-byte aligned unless said otherwise, no
  * allocation, no synchronisation, asynchronous on `stream`, arguments checked
@@ -52,7 +52,7 @@ int moe_i4_dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t
  *   [N][K/2] and ws as moe_i4_quantize writes them, rows ldw bytes (a multiple
  *   of 16) and lds elements apart; bias [N] float32 or NULL; y [M][N] MOE_BF16
  *   or MOE_F32 as `dtype`, rows ldy >= N elements apart.  K a multiple of 8;
- *   any M >= 0 (meant for few: for hundreds of rows
+ *   any M >= 0 (each 16 rows read the weights anew: for hundreds of rows
  *   dequantise them and use a bf16 product).  The nibbles and scales of a
  *   row's last 16 bytes past K are never used.
  *   Errors: MOE_ERR_INVALID_ARG for a NULL or misaligned pointer (ws 4-byte,
@@ -72,7 +72,8 @@ int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes);
 
 /* A1 to A7 for a decode step of T <= MOE_DECODE_MAX_T tokens: router logits,
  * selection (as moe_route, or moe_route_grouped with n_groups > 1), the local
- * experts' gate/up, SwiGLU and down, and the weighted sum, in one call.
+ * experts' gate/up, SwiGLU and down, and the weighted sum, in two kernels.
+ * Each expert's weights are read once for up to 16 of its tokens.
  *   x [T][d] bf16, Wr [E][d] bf16, bias [E] float32 or NULL; W1, W3 [NL][f][d]
  *   and W2 [NL][d][f] bf16; topk_idx [T][k] int32 and topk_w [T][k] float32,
  *   written (slots in falling order of the logits, ties to the lower expert);
@@ -91,7 +92,7 @@ int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes);
  *   Errors: MOE_ERR_INVALID_ARG for a NULL or misaligned pointer or a bad
  *   descriptor or n_groups (as moe_route_grouped); MOE_ERR_WORKSPACE for too
  *   small a workspace; MOE_ERR_UNSUPPORTED for more tokens, another dtype than
- *   MOE_BF16, or d or f above 2^20. */
+ *   MOE_BF16, d or f above 2^20, or T k f of 2^30 or more. */
 int moe_decode(const moe_desc* desc, int n_groups, const void* x, const void* Wr, const float* bias, const void* W1,
                const void* W3, const void* W2, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
                void* stream);

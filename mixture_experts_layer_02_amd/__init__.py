@@ -754,7 +754,7 @@ def _decode(name, b, x, wr, weights, bias, routing, n_groups, *group):
 
 
 def decode(b: DecodeBuffers, x, wr, w1, w3, w2, bias=None, routing=None, n_groups=1):
-    """forward for up to DECODE_MAX_T tokens in one call (bf16): the router, the
+    """forward for up to DECODE_MAX_T tokens in two kernels (bf16): the router, the
     experts and the combine -> b.y, with the selection in b.topk_idx and b.topk_w.
     ``routing=(topk_idx, topk_w)`` device tensors skip the router (wr is not read)."""
     D = b.desc

@@ -533,8 +533,10 @@ int moe_i4_linear(int64_t M, int64_t N, int64_t K, int group, const void* x, int
 static int check_decode(const moe_desc* d) {
   int rc = check_desc(d);
   if (rc) return rc;
-  return d->T > MOE_DECODE_MAX_T || d->dtype != MOE_BF16 || d->d > 1 << 20 || d->f > 1 << 20 ? MOE_ERR_UNSUPPORTED
-                                                                                              : MOE_OK;
+  if (d->T > MOE_DECODE_MAX_T || d->dtype != MOE_BF16 || d->d > 1 << 20 || d->f > 1 << 20 ||
+      (int64_t)d->T * d->k * d->f >= 1 << 30)  // (h is addressed with 32-bit offsets)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 
 int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes) {

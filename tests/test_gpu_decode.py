@@ -22,7 +22,8 @@ import torch
 import mixture_experts_layer_02_amd as moe
 import oracle
 import synth
-from gpu_util import to_dev, to_host
+from gpu_util import to_host
+from launched import kernels
 
 pytestmark = pytest.mark.gpu
 
@@ -397,11 +398,12 @@ def test_decode_keeps_a_token_that_is_not_finite_to_itself(gpu, group):
     np.testing.assert_array_equal(b.topk_idx.cpu().numpy()[ok], c.idx[ok])
 
 
-def test_decode_is_the_same_on_every_call(gpu):
+def test_decode_is_two_kernels_and_the_same_on_every_call(gpu):
     for T, group in ((1, 0), (64, 0), (1, 32), (20, 128)):
         c = Case(T, 256, 128, 32, 4, 0, 32, 1, 1, group, seed=15)
         b = c.run()
         first = [t.clone() for t in (b.y, b.topk_idx, b.topk_w)]
+        assert 1 <= len(kernels(lambda: c.run(b))) <= 2
         for _ in range(20):
             b.ws.random_(0, 256)
             c.run(b)
