@@ -44,20 +44,21 @@ constexpr int SYNC_FLAGS = 64;  // sync[0]: the counter of workgroups; sync[SYNC
 // ---------------------------------------------------------------------------
 
 // Partial sums part[ks][t][e] of x Wr^T: a workgroup has 16 experts and a
-// gridDim.y-th of d, a wave a quarter of that; 16 CT tokens.  Clears the second
+// gridDim.y-th of d, each of its 16 waves a sixteenth of that; 16 CT tokens.  Clears the second
 // kernel's counter and flags.
 template <int CT>
-__global__ void __launch_bounds__(256) decode_router_kernel(const uint16_t* __restrict__ x,
+__global__ void __launch_bounds__(1024) decode_router_kernel(const uint16_t* __restrict__ x,
                                                             const uint16_t* __restrict__ wr, int T, int d, int E,
                                                             float* __restrict__ part, uint32_t* __restrict__ sync,
                                                             int nsync) {
   typedef float f32x4_t __attribute__((ext_vector_type(4)));
-  __shared__ float red[4][CT * 16][17];
+  constexpr int W = 16;
+  __shared__ float red[W][CT * 16][17];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
   if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int i = tid; i < nsync; i += 256) sync[i] = 0;
+    for (int i = tid; i < nsync; i += 64 * W) sync[i] = 0;
   if (!wr) return;  // (the routing is given)
-  const int steps = d / 32, parts = gridDim.y * 4, me = blockIdx.y * 4 + wave;
+  const int steps = d / 32, parts = gridDim.y * W, me = blockIdx.y * W + wave;
   const int s0 = steps * me / parts, s1 = steps * (me + 1) / parts;
   const uint16_t* a = wr + (int64_t)min((int)blockIdx.x * 16 + r, E - 1) * d + q * 8;
   const uint16_t* b[CT];
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(256) decode_router_kernel(const uint16_t* __re
     b[c] = x + (int64_t)min(c * 16 + r, T - 1) * d + q * 8;
     acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  constexpr int U = CT == 1 ? 6 : 2;  // steps whose loads are in flight together
+  constexpr int U = CT == 1 ? 4 : 2;  // steps whose loads are in flight together
   for (int s = s0; s < s1; s += U) {
     bf16x8 fa[U], fb[U][CT];
 #pragma unroll
@@ -88,11 +89,12 @@ __global__ void __launch_bounds__(256) decode_router_kernel(const uint16_t* __re
 #pragma unroll
     for (int i = 0; i < 4; ++i) red[wave][c * 16 + r][4 * q + i] = acc[c][i];
   __syncthreads();
-  for (int i = tid; i < CT * 256; i += 256) {
+  for (int i = tid; i < CT * 256; i += 64 * W) {
     const int t = i >> 4, e = (int)blockIdx.x * 16 + (i & 15);
-    if (t < T && e < E)
-      part[((int64_t)blockIdx.y * T + t) * E + e] =
-          (red[0][t][i & 15] + red[1][t][i & 15]) + (red[2][t][i & 15] + red[3][t][i & 15]);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += red[w][t][i & 15];
+    if (t < T && e < E) part[((int64_t)blockIdx.y * T + t) * E + e] = sum;
   }
 }
 
@@ -121,40 +123,109 @@ struct alignas(8) Block {
   uint8_t off, nb; // which of the expert's blocks it is, and of how many
 };
 
-template <int MAXV>
-__device__ __forceinline__ void route_token(const DecodeParams& p, int t, int lane, int32_t* idx, float* w, int32_t* si,
-                                            float* sv) {
-  float v[MAXV];
-#pragma unroll
-  for (int i = 0; i < MAXV; ++i) v[i] = i * 64 + lane < p.E ? (p.bias ? p.bias[i * 64 + lane] : 0.f) : -INFINITY;
-  for (int s = 0; s < p.ks; ++s) {
-    const float* row = p.part + ((int64_t)s * p.T + t) * p.E;
-#pragma unroll
-    for (int i = 0; i < MAXV; ++i)
-      if (i * 64 + lane < p.E) v[i] += row[i * 64 + lane];
-  }
-  if (p.n_groups > 1) topk_rounds<MAXV, true>(v, lane, t, p.E, p.k, p.renorm, p.n_groups, idx, w);
-  else topk_token<MAXV>(v, lane, t, p.E, p.k, p.renorm, idx, w, si, sv);
+// Largest of the wave's values (none below 0), by moves along and across the rows of 16 lanes.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_max_dpp(uint32_t v) {
+  v = dpp_max<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8: lane 15 of a row has the row's
+  v = dpp_max<0x112, 0xf>(v);
+  v = dpp_max<0x114, 0xf>(v);
+  v = dpp_max<0x118, 0xf>(v);
+  v = dpp_max<0x142, 0xa>(v);  // row_bcast:15, :31: lane 63 has the wave's
+  v = dpp_max<0x143, 0xc>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// GRP 0: bf16 weights.  TMAX tokens at most, RB of them in a pass.  R1 rows (half
-// gate, half up) by 128 bytes a stage in phase 1, R2 by SUB2 times 128 in phase 2.
-template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int S>
+// The selection of token t by one wave, as moe_route and moe_route_grouped
+// define it, to idx and w ([k], LDS).  keys: the wave's E words of LDS.  Per group
+// of experts its best k / n_groups one after the other: lane l keeps the best of
+// the group's experts l, l + 64, ...; the wave's best is found over the lanes, and
+// its lane looks through its experts again.  Short code rather than few steps: it
+// runs once per launch, from a cold instruction cache (with a token's logits in
+// registers, unrolled for up to 16 a lane, the kernel was 128 KB long, and 12
+// tokens in 4 groups took 20 us; so, 4).
+__device__ __forceinline__ void route_token(const DecodeParams& p, int t, int lane, uint32_t* keys, int32_t* idx,
+                                            float* w) {
+  for (int e = lane; e < p.E; e += 64) {
+    float v = p.bias ? p.bias[e] : 0.f;
+    const float* row = p.part + (int64_t)t * p.E + e;
+    if (p.ks == 1) v += row[0];
+    else {
+      const int64_t ld = (int64_t)p.T * p.E;
+      v += (row[0] + row[ld]) + (row[2 * ld] + row[3 * ld]);
+    }
+    keys[e] = max(order_key(v), 1u);  // 0: taken
+  }
+  const int Eg = p.E / p.n_groups, kg = p.k / p.n_groups;
+  uint32_t my_key = 0, my_i = 0;  // lane j: pick j
+  for (int g = 0, j = 0; g < p.n_groups; ++g) {
+    const uint32_t* kg_p = keys + g * Eg;
+    uint32_t best = 0, at = 0;
+    auto look = [&]() {
+      best = 0;
+      for (int e = lane; e < Eg; e += 64) {
+        const uint32_t v = kg_p[e];
+        if (v > best) best = v, at = e;
+      }
+    };
+    look();
+    for (int r = 0; r < kg; ++r, ++j) {
+      const uint32_t top = wave_max_dpp(best);
+      const uint32_t e = ~wave_max_dpp(best == top ? ~at : 0u);  // the lowest of equals
+      if (lane == j) my_key = top, my_i = g * Eg + e;
+      if (lane == (int)(e & 63)) {
+        keys[g * Eg + e] = 0;
+        look();
+      }
+    }
+  }
+  // Slots in falling order: pick j's is the number of picks before it.
+  int rank = 0;
+  uint32_t first = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t kj = (uint32_t)__builtin_amdgcn_readlane((int)my_key, j);
+    const uint32_t ij = (uint32_t)__builtin_amdgcn_readlane((int)my_i, j);
+    rank += kj > my_key || (kj == my_key && ij < my_i);
+    first = max(first, kj);
+  }
+  const float v0 = key_float(first);
+  float sum = 0.f;
+  const float ex = expf(key_float(my_key) - v0);
+  if (p.renorm) {
+    sum = lane < p.k ? ex : 0.f;
+  } else {
+    if (lane < p.k) keys[my_i] = my_key;
+    __builtin_amdgcn_wave_barrier();
+    for (int e = lane; e < p.E; e += 64) sum += expf(key_float(keys[e]) - v0);
+  }
+  sum = wave_sum(sum);
+  if (lane < p.k) {
+    idx[rank] = (int)my_i;
+    w[rank] = ex / sum;
+  }
+}
+
+// GRP 0: bf16 weights.  TMAX tokens at most, RB of them in a pass over an expert's
+// rows.  R1 rows (half gate, half up) a stage in phase 1, R2 by SUB2 pieces of 128
+// bytes in phase 2; W streaming waves with RINGW bytes of ring each.
+template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int RINGW>
 __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   using namespace stream;
   using ST1 = Stage<GRP, R1, 1, true, RB>;
   using ST2 = Stage<GRP, R2, SUB2, false, RB>;
-  constexpr int SLOT = ST1::BYTES > ST2::BYTES ? ST1::BYTES : ST2::BYTES;
-  constexpr int PER1 = ST1::WI + ST1::SI + ST1::XI, PRE2 = ST2::WI + ST2::SI, PER2 = PRE2 + ST2::XI;
+  constexpr int S1 = RINGW / ST1::BYTES < 8 ? RINGW / ST1::BYTES : 8, S2 = RINGW / ST2::BYTES < 8 ? RINGW / ST2::BYTES : 8;
+  constexpr int PRE1 = ST1::WI + ST1::SI, PRE2 = ST2::WI + ST2::SI;  // copies of a stage's weights
   constexpr int RP = R1 + 4;  // pitch of phase 1's partial sums (floats)
   constexpr int RED = 2 * W * RB * RP * 4, YACC = W * TMAX * R2 * 4, ACC = RED > YACC ? RED : YACC;
-  constexpr int RING = W * S * SLOT;
+  constexpr int RING = W * RINGW, NT = 64 * (W + 1);
   constexpr int ROWS = TMAX * MAX_K, BLOCKS = TMAX <= RB ? (ROWS < MAX_E ? ROWS : MAX_E) : MAX_E + ROWS / RB;
   // Scratch of the selection, over the ring before it starts.
   constexpr int O_IDX = 0, O_W = O_IDX + ROWS * 4, O_MASK = O_W + ROWS * 4, O_BASE = O_MASK + MAX_E * 8,
-                O_TOP = O_BASE + MAX_E * 2, SCRATCH = O_TOP + (W + 1) * 512;
+                O_KEY = O_BASE + MAX_E * 2, SCRATCH = O_KEY + (W + 1) * MAX_E * 4;
   static_assert(SCRATCH <= RING, "scratch");
-  static_assert((S - 1) * PER1 < 64 && (S - 1) * PER2 < 64, "vmcnt");
+  static_assert(S1 >= 2 && S2 >= 2, "stages");
   __shared__ __attribute__((aligned(1024))) uint8_t ring_m[RING];
   __shared__ __attribute__((aligned(16))) uint8_t acc_m[ACC];
   __shared__ Block s_blk[BLOCKS];
@@ -172,37 +243,30 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   float* l_w = reinterpret_cast<float*>(ring_m + O_W);
   unsigned long long* l_mask = reinterpret_cast<unsigned long long*>(ring_m + O_MASK);
   uint16_t* l_base = reinterpret_cast<uint16_t*>(ring_m + O_BASE);
-  if (tid == 64 * W)
-    s_vid = (int)__hip_atomic_fetch_add(p.sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int i = tid; i < slots; i += 64 * (W + 1)) {
-    // (a token whose logits are not numbers may leave slots unwritten)
-    l_idx[i] = p.part ? i % p.k : p.idx[i];
-    l_w[i] = p.part ? __uint_as_float(0x7fc00000u) : p.w[i];
-  }
-  for (int i = tid; i < p.NL; i += 64 * (W + 1)) l_mask[i] = 0;
-  __syncthreads();
+  int number = 0;
+  if (tid == 64 * W) number = (int)__hip_atomic_fetch_add(p.sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = tid; i < p.NL; i += NT) l_mask[i] = 0;
   if (p.part) {
-    int32_t* si = reinterpret_cast<int32_t*>(ring_m + O_TOP + wave * 512);
-    float* sv = reinterpret_cast<float*>(si + 64);
-    for (int t = wave; t < p.T; t += W + 1) {
-      if (p.E <= 64) route_token<1>(p, t, lane, l_idx, l_w, si, sv);
-      else if (p.E <= 128) route_token<2>(p, t, lane, l_idx, l_w, si, sv);
-      else if (p.E <= 384) route_token<6>(p, t, lane, l_idx, l_w, si, sv);
-      else route_token<16>(p, t, lane, l_idx, l_w, si, sv);
-    }
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int i = tid; i < slots; i += 64 * (W + 1)) p.idx[i] = l_idx[i], p.w[i] = l_w[i];
+    uint32_t* keys = reinterpret_cast<uint32_t*>(ring_m + O_KEY) + wave * MAX_E;
+#pragma nounroll
+    for (int t = wave; t < p.T; t += W + 1) route_token(p, t, lane, keys, l_idx + t * p.k, l_w + t * p.k);
+  } else {
+    for (int i = tid; i < slots; i += NT) l_idx[i] = p.idx[i], l_w[i] = p.w[i];
   }
+  if (tid == 64 * W) s_vid = number;
+  __syncthreads();
+  if (p.part && blockIdx.x == 0)
+    for (int i = tid; i < slots; i += NT) p.idx[i] = l_idx[i], p.w[i] = l_w[i];
   const int vid = __builtin_amdgcn_readfirstlane(s_vid);
   if (vid >= G) return;  // (another workgroup has done this one's items)
-  for (int i = tid; i < slots; i += 64 * (W + 1)) {
+  for (int i = tid; i < slots; i += NT) {
     const uint32_t e = (uint32_t)l_idx[i] - (uint32_t)p.e0;
     if (e < (uint32_t)p.NL) atomicOr(&l_mask[e], 1ull << (i / p.k));
   }
   __syncthreads();
   if (wave == 0) {  // exclusive sums of the experts' rows and blocks, 64 experts at a time
     uint32_t before = 0;
+#pragma nounroll
     for (int base = 0; base < p.NL; base += 64) {
       const int e = base + lane;
       const int n = e < p.NL ? __popcll(l_mask[e]) : 0, nb = (n + RB - 1) / RB;
@@ -223,7 +287,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     if (lane == 0) s_nblk = (int)(before >> 16);
   }
   __syncthreads();
-  for (int i = tid; i < slots; i += 64 * (W + 1)) {
+  for (int i = tid; i < slots; i += NT) {
     const uint32_t e = (uint32_t)l_idx[i] - (uint32_t)p.e0;
     if (e >= (uint32_t)p.NL) continue;
     const int t = i / p.k;
@@ -245,10 +309,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   // ---- items
   constexpr int PR1 = R1 / 2;
   const int nblk = __builtin_amdgcn_readfirstlane(s_nblk);
-  const int tiles1 = p.f / PR1, n1 = nblk * tiles1, n2 = p.d / R2;
-  const int C1 = (p.d + ST1::KS - 1) / ST1::KS, C2 = (p.f + ST2::KS - 1) / ST2::KS;  // stages of a row
-  const int64_t pitch1 = GRP ? p.d / 2 : (int64_t)p.d * 2, pitch2 = GRP ? p.f / 2 : (int64_t)p.f * 2;
-  const int groups1 = GRP ? (p.d + GRP - 1) / (GRP ? GRP : 1) : 0, groups2 = GRP ? (p.f + GRP - 1) / (GRP ? GRP : 1) : 0;
+  const int tiles1 = p.f / PR1, n1 = nblk * tiles1, n2 = (p.d + R2 - 1) / R2;
+  auto count = [&](int first, int n) { return first < n ? (n - 1 - first) / G + 1 : 0; };  // items first, first + G, ..
   auto block = [&](int b) {  // (uniform)
     const u32x2_t v = *reinterpret_cast<const u32x2_t*>(&s_blk[b]);
     return __builtin_bit_cast(Block, u32x2_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)v[0]),
@@ -258,9 +320,12 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   auto item1 = [&](int i, Block& b, int& tile) {
     const int bi = i / tiles1;
     b = block(bi);
-    const int b0 = bi - b.off, local = i - b0 * tiles1;
-    tile = local / b.nb;
-    b = block(b0 + local % b.nb);
+    tile = i - bi * tiles1;
+    if (TMAX > RB && b.nb > 1) {
+      const int b0 = bi - b.off, local = i - b0 * tiles1;
+      tile = local / b.nb;
+      b = block(b0 + local % b.nb);
+    }
   };
 
   float* red = reinterpret_cast<float*>(acc_m);
@@ -270,7 +335,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 
   // Sums of an item of phase 2 over the waves, and their stores.
   auto store_y = [&](int tile) {
-    for (int i = tid; i < p.T * (R2 / 2); i += 64 * (W + 1)) {
+    const int chans = min(R2, p.d - tile * R2);
+    for (int i = tid; i < p.T * (R2 / 2); i += NT) {
       const int t = i / (R2 / 2), c = (i % (R2 / 2)) * 2;
       float a = 0.f, b = 0.f;
 #pragma unroll
@@ -278,13 +344,15 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         a += yacc[(w * p.T + t) * R2 + c];
         b += yacc[(w * p.T + t) * R2 + c + 1];
       }
-      *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.d + tile * R2 + c) = lost ? 0x7fc07fc0u : pack_bf2(a, b);
+      if (c < chans)
+        *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.d + tile * R2 + c) = lost ? 0x7fc07fc0u : pack_bf2(a, b);
     }
   };
 
   if (wave == W) {  // ---- the serving wave
     bool take = true;
     for (int cur = vid;;) {
+#pragma nounroll
       for (int item = cur, n = 0; item < n1; item += G, ++n) {
         Block b;
         int tile;
@@ -306,7 +374,10 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+      // h was stored past the XCD's L2 (atomic, at agent scope), so its stores being
+      // complete is enough: a release fence writes back the whole L2, which took
+      // 1 to 6 us with the CUs of an XCD at it together.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       if (lane == 0)
         __hip_atomic_store(p.sync + SYNC_FLAGS + cur, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       // All flags up: on.  Else, after 20 us, take the number of a workgroup that
@@ -335,7 +406,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
           cmd = -2;
           break;
         }
-        __builtin_amdgcn_s_sleep(2);
+        __builtin_amdgcn_s_sleep(1);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       if (lane == 0) {
@@ -359,196 +430,215 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   }
 
   // ---- a streaming wave
-  const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring_m) + wave * S * SLOT;
-  const uint8_t* ring_p = ring_m + wave * S * SLOT;
-  // What is copied next: phase (3: nothing), item, block, stage.
-  int c_ph = 1, c_item = vid, c_blk = 0, c_st = wave, c_step = G;
-  bool c_new = true, c_on = true, h_there = false;  // c_on: phase 2 follows
-  Source src;
-  uint32_t xr1[ST1::XI], xr2[ST2::XI];
-  int head = 0, tail = 0, flying = 0;  // ring slots; stages in flight
+  const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring_m) + wave * RINGW;
+  const uint8_t* ring_p = ring_m + wave * RINGW;
+  Ages ages;
 
-  auto source1 = [&]() {
-    Block b;
-    int tile;
-    item1(c_item, b, tile);
-    const int64_t row = (int64_t)b.e * p.f + tile * PR1;
-    src.w[0] = make_rsrc(p.w1 + row * pitch1, PR1 * pitch1);
-    src.w[1] = make_rsrc(p.w3 + row * pitch1, PR1 * pitch1);
-    if (GRP) {
-      src.s[0] = make_rsrc(p.s1 + row * groups1, (uint64_t)PR1 * groups1 * 4);
-      src.s[1] = make_rsrc(p.s3 + row * groups1, (uint64_t)PR1 * groups1 * 4);
-    }
-    src.x = make_rsrc(p.x, (uint64_t)p.T * p.d * 2);
-    src.pitch = (uint32_t)pitch1, src.spitch = groups1 * 4, src.K = p.d, src.rows = PR1;
-#pragma unroll
-    for (int n = 0; n < ST1::XI; ++n) {
-      const int row = ST1::x_row(n, lane);
-      xr1[n] = row < b.n ? (uint32_t)(s_row[b.pos + row] / p.k) * (uint32_t)p.d * 2 : NOWHERE;
-    }
-  };
+  // Phase 2's share: of the item's stages (blocks by stages of a row of f) a
+  // stretch, the same in every item.
+  const int C2 = (p.f + ST2::KS - 1) / ST2::KS, q0 = nblk * C2 * wave / W, per2 = nblk * C2 * (wave + 1) / W - q0;
+  const int blk2 = q0 / C2, st2 = q0 - blk2 * C2;  // where it starts
+  Source src;
+  uint32_t xr2[ST2::XI];
+  int rows2 = 0;
   auto source2 = [&](int item, int blk) {
+    const int64_t pitch = GRP ? p.f / 2 : (int64_t)p.f * 2;
     const Block b = block(blk);
     const int64_t row = (int64_t)b.e * p.d + item * R2;
-    src.w[0] = make_rsrc(p.w2 + row * pitch2, R2 * pitch2);
-    if (GRP) src.s[0] = make_rsrc(p.s2 + row * groups2, (uint64_t)R2 * groups2 * 4);
+    src.rows = min(R2, p.d - item * R2);
+    src.w[0] = make_rsrc(p.w2 + row * pitch, src.rows * pitch);
+    src.pitch = (uint32_t)pitch;
+    if (GRP) {
+      const int groups = (p.f + GRP - 1) / (GRP ? GRP : 1);
+      src.s[0] = make_rsrc(p.s2 + row * groups, (uint64_t)src.rows * groups * 4);
+      src.spitch = groups * 4;
+    }
     src.x = make_rsrc(p.h, (uint64_t)slots * p.f * 2);
-    src.pitch = (uint32_t)pitch2, src.spitch = groups2 * 4, src.K = p.f, src.rows = R2;
+    src.K = p.f;
+    rows2 = b.n;
 #pragma unroll
-    for (int n = 0; n < ST2::XI; ++n) {
-      const int row = ST2::x_row(n, lane);
-      xr2[n] = row < b.n ? (uint32_t)s_row[b.pos + row] * (uint32_t)p.f * 2 : NOWHERE;
-    }
+    for (int n = 0; n < ST2::XI; ++n)
+      xr2[n] = (uint32_t)s_row[b.pos + min(ST2::x_row(n, lane), b.n - 1)] * (uint32_t)p.f * 2;
   };
-  // To the next stage of phase 2 that this wave has; false past the last item.
-  auto settle2 = [&](int& item, int& blk, int& st, bool& fresh) {
-    if (nblk == 0) return false;
-    while (item < n2 && st >= C2) {
-      st -= C2;
-      fresh = true;
-      if (++blk == nblk) blk = 0, st = wave, item += c_step;
-    }
-    return item < n2;
-  };
-  auto copy_next = [&]() {
-    if (c_ph == 1) {
-      while (c_item < n1 && c_st >= C1) c_item += G, c_st = wave, c_new = true;
-      if (c_item >= n1) c_ph = c_on ? 2 : 3, c_item = vid, c_blk = 0, c_st = wave, c_new = true;
-    }
-    if (c_ph == 2 && !settle2(c_item, c_blk, c_st, c_new)) c_ph = 3;
-    if (c_ph == 3) return;
-    const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * SLOT);
-    if (c_ph == 1) {
-      if (c_new) source1();
-      const int k0 = __builtin_amdgcn_readfirstlane(c_st * ST1::KS);
-      ST1::copy_w(src, k0, at, lane);
-      ST1::copy_x(src, xr1, k0, at, lane);
-    } else {
-      if (c_new) source2(c_item, c_blk);
-      const int k0 = __builtin_amdgcn_readfirstlane(c_st * ST2::KS);
-      ST2::copy_w(src, k0, at, lane);
-      if (h_there) ST2::copy_x(src, xr2, k0, at, lane);
-    }
+  // The stage to copy next in phase 2.
+  int c_item = vid, c_blk = blk2, c_st = st2, c_left = per2;
+  bool c_new = true;
+  auto next2 = [&]() {
     c_new = false;
-    c_st += W;
-    head = head + 1 == S ? 0 : head + 1;
-    ++flying;
-  };
-  auto taken = [&]() {
-    tail = tail + 1 == S ? 0 : tail + 1;
-    --flying;
+    if (--c_left == 0) c_left = per2, c_item += G, c_blk = blk2, c_st = st2, c_new = true;
+    else if (++c_st == C2) c_st = 0, ++c_blk, c_new = true;
   };
 
-  for (int i = 0; i < S; ++i) copy_next();
+  int ahead = 0;  // stages of phase 2 whose weights were asked for before all of h was there
   for (int cur = vid;;) {
-    for (int item = cur, n = 0; item < n1; item += G, ++n) {
+    // Phase 1: the wave has a stretch of d in every item.
+    const int C1 = (p.d + ST1::KS - 1) / ST1::KS, s0 = C1 * wave / W, per1 = C1 * (wave + 1) / W - s0;
+    const int items = count(cur, n1);
+    if (per1 == 0) {
+#pragma nounroll
+      for (int n = 0; n < items; ++n) {
+        float* rd = red + ((n & 1) * W + wave) * RB * RP;
+        for (int i = lane; i < RB * RP; i += 64) rd[i] = 0.f;
+        lds_barrier();
+      }
+    } else {
+      uint32_t xr1[ST1::XI];
+      int rows1 = 0, c_at = 0, c_i = cur;     // copied next: stage of the item, item
+      int u_at = 0, u_n = 0, head = 0, tail = 0;  // used next: stage of the item, item's place; ring slots
       f32x4_t acc[ST1::RT];
 #pragma unroll
       for (int t = 0; t < ST1::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      for (int st = wave; st < C1; st += W) {
-        // the oldest stage has landed when no more than the S - 1 younger ones' copies are outstanding
-        if (flying < S) wait_vm<0>();
-        else if (c_ph == 1) wait_vm<(S - 1) * PER1>();
-        else wait_vm<(S - 1) * (PRE2 < PER1 ? PRE2 : PER1)>();
-        asm volatile("" ::: "memory");
-        ST1 s;
-        s.read(ring_p + tail * SLOT, lane);
-        reads_done();
-        taken();
-        copy_next();
-        s.multiply(acc);
-      }
-      float* rd = red + ((n & 1) * W + wave) * RB * RP;
-      if (r < RB) {
+      src.pitch = (uint32_t)(GRP ? p.d / 2 : p.d * 2);
+      src.K = p.d, src.rows = PR1;
+      src.x = make_rsrc(p.x, (uint64_t)p.T * p.d * 2);
+#pragma nounroll
+      while (u_n < items) {
+        const bool copies = c_i < n1, use = ages.n == S1 || !copies;
+        if (use) {
+          ages.pop();
+          wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
+          ST1 s;
+          s.read(ring_p + tail * ST1::BYTES, lane);
+          s.multiply(acc);
+          reads_done();
+          tail = tail + 1 == S1 ? 0 : tail + 1;
+        }
+        if (copies) {
+          if (c_at == 0) {
+            Block b;
+            int tile;
+            item1(c_i, b, tile);
+            const int64_t row = (int64_t)b.e * p.f + tile * PR1, pitch = GRP ? p.d / 2 : (int64_t)p.d * 2;
+            src.w[0] = make_rsrc(p.w1 + row * pitch, PR1 * pitch);
+            src.w[1] = make_rsrc(p.w3 + row * pitch, PR1 * pitch);
+            if (GRP) {
+              const int groups = (p.d + GRP - 1) / (GRP ? GRP : 1);
+              src.s[0] = make_rsrc(p.s1 + row * groups, (uint64_t)PR1 * groups * 4);
+              src.s[1] = make_rsrc(p.s3 + row * groups, (uint64_t)PR1 * groups * 4);
+              src.spitch = groups * 4;
+            }
+            rows1 = b.n;
 #pragma unroll
-        for (int t = 0; t < ST1::RT; ++t) *reinterpret_cast<f32x4_t*>(rd + r * RP + 16 * t + 4 * q) = acc[t];
+            for (int n = 0; n < ST1::XI; ++n)
+              xr1[n] = (uint32_t)(s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] / p.k) * (uint32_t)p.d * 2;
+          }
+          const int k0 = (s0 + c_at) * ST1::KS;
+          const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST1::BYTES);
+          ST1::copy_w(src, k0, at, lane);
+          ages.push(PRE1 + ST1::copy_x(src, xr1, rows1, k0, at, lane));
+          head = head + 1 == S1 ? 0 : head + 1;
+          if (++c_at == per1) c_at = 0, c_i += G;
+        }
+        if (use) {
+          if (++u_at == per1) {
+            float* rd = red + ((u_n & 1) * W + wave) * RB * RP;
+            if (r < RB) {
+#pragma unroll
+              for (int t = 0; t < ST1::RT; ++t) *reinterpret_cast<f32x4_t*>(rd + r * RP + 16 * t + 4 * q) = acc[t];
+            }
+#pragma unroll
+            for (int t = 0; t < ST1::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            u_at = 0;
+            ++u_n;
+            lds_barrier();
+          }
+        }
       }
-      lds_barrier();
+    }
+    // The weights of phase 2's first stages, while the other workgroups finish theirs.
+    if (cur == vid) {
+      ahead = min(S2, count(vid, n2) * per2);
+#pragma nounroll
+      for (int i = 0; i < ahead; ++i) {
+        if (c_new) source2(c_item, c_blk);
+        ST2::copy_w(src, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring + i * ST2::BYTES), lane);
+        next2();
+      }
     }
     lds_barrier();  // (1)
     const int cmd = __builtin_amdgcn_readfirstlane(s_cmd);
     lost = cmd == -2;
     if (cmd < 0) break;
-    // A number taken over: what was copied ahead for phase 2 is dropped.
-    ++nmore;
+    ++nmore;  // a number taken over; what was copied ahead is dropped
     cur = cmd;
     lds_barrier();  // (2)
     wait_vm<0>();
     asm volatile("" ::: "memory");
-    head = tail = flying = 0;
-    c_ph = 1, c_item = cur, c_blk = 0, c_st = wave, c_new = true, c_on = false;
-    for (int i = 0; i < S; ++i) copy_next();
+    ahead = 0;
   }
 
-  // Phase 2.  The stages in flight, if any, are its first ones without their rows of h.
-  h_there = true;
-  int late = 0;  // stages whose rows of h were copied after the weights of all in flight
-  if (c_on) {
-    const int ahead = flying;
-    int item = vid, blk = 0, st = wave;
-    for (int i = 0; i < ahead; ++i) {
-      bool fresh = true;
-      settle2(item, blk, st, fresh);
-      source2(item, blk);
-      ST2::copy_x(src, xr2, __builtin_amdgcn_readfirstlane(st * ST2::KS),
-                  __builtin_amdgcn_readfirstlane(ring + ((tail + i) % S) * SLOT), lane);
-      st += W;
-    }
-    late = ahead;
-    c_new = true;
-  }
+  // Phase 2.
+#pragma nounroll
   for (int l = 0; l <= nmore; ++l) {
     const int first = __builtin_amdgcn_readfirstlane(l ? (int)s_more[l - 1] : vid);
-    if (l > 0 || !c_on) {
-      c_ph = 2, c_item = first, c_blk = 0, c_st = wave, c_new = true;
-      head = tail = flying = 0;
-      for (int i = 0; i < S; ++i) copy_next();
+    c_item = first, c_blk = blk2, c_st = st2, c_left = per2, c_new = true;
+    int head = 0, tail = 0;
+#pragma nounroll
+    for (; head < ahead; ++head) {  // their rows of h
+      if (c_new) source2(c_item, c_blk);
+      ages.push(ST2::copy_x(src, xr2, rows2, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring + head * ST2::BYTES), lane));
+      next2();
     }
-    for (int item = first; item < n2; item += G) {
-      float* mine = yacc + wave * p.T * R2;
+    ahead = 0;
+    if (head == S2) head = 0;
+    const int items = count(first, n2);
+    int copies = items * per2 - ages.n;  // stages that are still to be copied
+    float* mine = yacc + wave * p.T * R2;
+#pragma nounroll
+    for (int n = 0; n < items; ++n) {
       for (int i = lane; i < p.T * R2; i += 64) mine[i] = 0.f;
-      f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-      int have = -1;
-      auto flush = [&]() {  // the block's products, times the routing weights, to their tokens
-        if (have < 0) return;
-        const Block b = block(have);
-        if (r < b.n && (R2 > 8 || q < 2)) {
-          const int slot = s_row[b.pos + r];
-          const float w = s_roww[b.pos + r];
-          f32x4_t* to = reinterpret_cast<f32x4_t*>(mine + (slot / p.k) * R2 + 4 * q);
-          f32x4_t v = *to;
+      f32x4_t acc[ST2::RT];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += w * acc[0][i];
-          *to = v;
+      for (int t = 0; t < ST2::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      int blk = blk2, st = st2;
+#pragma nounroll
+      for (int left = per2; left > 0;) {
+        const bool use = ages.n == S2 || copies == 0;
+        if (use) {
+          ages.pop();
+          wait_younger<(S2 - 1) * (PRE2 + 1)>(ages.sum);
+          ST2 s;
+          s.read(ring_p + tail * ST2::BYTES, lane);
+          s.multiply(acc);
+          reads_done();
+          tail = tail + 1 == S2 ? 0 : tail + 1;
         }
-        acc[0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      };
-      for (int blk = 0, st = wave; blk < nblk;) {
-        if (st >= C2) {
-          st -= C2;
-          ++blk;
-          continue;
+        if (copies > 0) {
+          if (c_new) source2(c_item, c_blk);
+          const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST2::BYTES);
+          const int k0 = c_st * ST2::KS;
+          ST2::copy_w(src, k0, at, lane);
+          ages.push(PRE2 + ST2::copy_x(src, xr2, rows2, k0, at, lane));
+          next2();
+          head = head + 1 == S2 ? 0 : head + 1;
+          --copies;
         }
-        if (blk != have) {
-          flush();
-          have = blk;
+        if (use) {
+          --left;
+          if (++st == C2 || left == 0) {  // the block's products, times the routing weights, to their tokens
+            const Block b = block(blk);
+            if (r < b.n) {
+              const int slot = s_row[b.pos + r];
+              const float w = s_roww[b.pos + r];
+              float* to = mine + (slot / p.k) * R2 + 4 * q;
+#pragma unroll
+              for (int t = 0; t < ST2::RT; ++t)
+                if (R2 - 16 * t >= 16 || q < 2) {
+                  f32x4_t v = *reinterpret_cast<f32x4_t*>(to + 16 * t);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) v[i] += w * acc[t][i];
+                  *reinterpret_cast<f32x4_t*>(to + 16 * t) = v;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < ST2::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            st = 0;
+            ++blk;
+          }
         }
-        if (flying < S) wait_vm<0>();
-        else if (late > 0) wait_vm<(S - 1) * ST2::XI>();
-        else wait_vm<(S - 1) * PER2>();
-        late -= late > 0;
-        asm volatile("" ::: "memory");
-        ST2 s;
-        s.read(ring_p + tail * SLOT, lane);
-        reads_done();
-        taken();
-        copy_next();
-        s.multiply(acc);
-        st += W;
       }
-      flush();
       lds_barrier();
-      store_y(item);
+      store_y(first + n * G);
       lds_barrier();
     }
   }
@@ -557,27 +647,34 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 // ---------------------------------------------------------------------------
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
-// Parts of d in the logits' partial sums: more of them spread the router's
-// weights over more CUs, but every workgroup of the second kernel reads all.
-int router_parts(const moe_desc& d) { return d.T <= 4 ? 8 : 2; }
+// Parts of d in the logits' partial sums (1 or 4, see route_token): more of them
+// spread the router's weights over more CUs, but every workgroup of the second
+// kernel reads all.
+int router_parts(const moe_desc& d) { return d.T <= 8 && d.d >= 1024 ? 4 : 1; }
 int64_t part_bytes(const moe_desc& d) { return align256((int64_t)router_parts(d) * d.T * d.E * 4); }
 constexpr int64_t SYNC_BYTES = 4096;
 constexpr int MAX_WGS = SYNC_BYTES / 4 - SYNC_FLAGS;
 
-template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int S>
+template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int RINGW>
 hipError_t run(const DecodeParams& p, int grid, hipStream_t s) {
-  decode_kernel<GRP, TMAX, RB, R1, R2, SUB2, W, S><<<(unsigned)grid, 64 * (W + 1), 0, s>>>(p);
+  decode_kernel<GRP, TMAX, RB, R1, R2, SUB2, W, RINGW><<<(unsigned)grid, 64 * (W + 1), 0, s>>>(p);
   return hipGetLastError();
 }
 
 template <int GRP>
 hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
+  // Channels of d an item: 24 where that leaves no workgroup with more than 8 would.
+  auto busiest = [&](int r2) { return ((p.d + r2 - 1) / r2 + grid - 1) / grid * r2; };
+  const bool wide = busiest(24) <= busiest(8);
   if constexpr (GRP == 0) {
-    if (p.T <= 2) return run<0, 2, 2, 16, 8, 2, 8, 6>(p, grid, s);
-    return run<0, MAX_T, 16, 16, 16, 1, 8, 3>(p, grid, s);
+    if (p.T <= 2) return wide ? run<0, 2, 2, 16, 24, 1, 8, 16384>(p, grid, s) : run<0, 2, 2, 16, 8, 3, 8, 16384>(p, grid, s);
+    if (p.T <= 16) return wide ? run<0, 16, 16, 16, 24, 1, 8, 16384>(p, grid, s) : run<0, 16, 16, 16, 8, 2, 8, 16384>(p, grid, s);
+    return wide ? run<0, MAX_T, 12, 16, 24, 1, 8, 10752>(p, grid, s) : run<0, MAX_T, 12, 16, 8, 2, 8, 10752>(p, grid, s);
   } else {
-    if (p.T <= 2) return run<GRP, 2, 2, 16, 8, 1, 8, 4>(p, grid, s);
-    return run<GRP, MAX_T, 16, 32, 16, 1, 4, 2>(p, grid, s);
+    constexpr int SMALL = GRP == 32 ? 14592 : 17408;
+    if (p.T <= 2) return wide ? run<GRP, 2, 2, 16, 24, 1, 8, SMALL>(p, grid, s) : run<GRP, 2, 2, 16, 8, 1, 8, SMALL>(p, grid, s);
+    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8, 16384>(p, grid, s);
+    return wide ? run<GRP, MAX_T, 8, 32, 24, 1, 4, 28672>(p, grid, s) : run<GRP, MAX_T, 8, 32, 8, 1, 4, 28672>(p, grid, s);
   }
 }
 
@@ -597,10 +694,10 @@ hipError_t launch_decode(const moe_desc& d, int group, int n_groups, const void*
   const int ks = router_parts(d);
   const dim3 rgrid = Wr ? dim3((unsigned)((d.E + 15) / 16), (unsigned)ks) : dim3(1, 1);
   if (d.T <= 16)
-    decode_router_kernel<1><<<rgrid, 256, 0, s>>>((const uint16_t*)x, (const uint16_t*)Wr, d.T, d.d, d.E, part, sync,
+    decode_router_kernel<1><<<rgrid, 1024, 0, s>>>((const uint16_t*)x, (const uint16_t*)Wr, d.T, d.d, d.E, part, sync,
                                                   SYNC_FLAGS + grid);
   else
-    decode_router_kernel<4><<<rgrid, 256, 0, s>>>((const uint16_t*)x, (const uint16_t*)Wr, d.T, d.d, d.E, part, sync,
+    decode_router_kernel<4><<<rgrid, 1024, 0, s>>>((const uint16_t*)x, (const uint16_t*)Wr, d.T, d.d, d.E, part, sync,
                                                   SYNC_FLAGS + grid);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -200,8 +200,7 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
   uint32_t xr[ST::XI];
 #pragma unroll
   for (int n = 0; n < ST::XI; ++n) {
-    const int row = ST::x_row(n, lane);
-    xr[n] = row < rows ? (uint32_t)(row * p.ldx * 2) : NOWHERE;
+    xr[n] = (uint32_t)(ST::x_row(n, lane) * p.ldx * 2);
   }
   const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * S * ST::BYTES;
   const uint8_t* ring_p = smem + wave * S * ST::BYTES;
@@ -211,8 +210,9 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
     const int k0 = __builtin_amdgcn_readfirstlane((wave + W * i) * 256);
     const uint32_t at = __builtin_amdgcn_readfirstlane(ring + slot * ST::BYTES);
     ST::copy_w(src, k0, at, lane);
-    ST::copy_x(src, xr, k0, at, lane);
+    ST::copy_x(src, xr, rows, k0, at, lane);
   };
+  const int per = ST::WI + ST::SI + (rows * ST::XROW + 1023) / 1024;  // copies of a stage
   f32x4_t acc[ST::RT];
 #pragma unroll
   for (int t = 0; t < ST::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -221,9 +221,7 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
     if (i < mine) copy(i, i);
   int slot = 0;
   for (int i = 0; i < mine; ++i) {
-    if (i + S <= mine) wait_vm<(S - 1) * (ST::WI + ST::SI + ST::XI)>();
-    else wait_vm<0>();
-    asm volatile("" ::: "memory");
+    wait_younger<(S - 1) * (ST::WI + ST::SI + ST::XI)>((min(i + S, mine) - i - 1) * per);
     ST st;
     st.read(ring_p + slot * ST::BYTES, lane);
     reads_done();

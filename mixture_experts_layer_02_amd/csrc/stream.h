@@ -44,8 +44,8 @@ struct Source {
   int K, rows;             // k in all; rows of a part that exist
 };
 
-// GRP 0: bf16 weights; else 4 bits with a scale per GRP.  R weight rows (8, or a
-// multiple of 16; DUAL: eight of the first matrix, eight of the second, and so
+// GRP 0: bf16 weights; else 4 bits with a scale per GRP.  R weight rows (a
+// multiple of 8; DUAL: eight of the first matrix, eight of the second, and so
 // on) by SUB pieces of 128 bytes, RB activation rows.
 template <int GRP, int R, int SUB, bool DUAL, int RB>
 struct Stage {
@@ -55,12 +55,11 @@ struct Stage {
   static constexpr int WB = R * SUB * 128, WI = WB / 1024;               // bytes; copies
   static constexpr int GPC = I4 ? KC / (I4 ? GRP : 1) : 0;               // groups of a stage
   static constexpr int SIP = (GPC * PR + 63) / 64, SI = SIP * PARTS, SB = SI * 256;
-  static constexpr int XROW = KC * 2, XB = SUB * RB * XROW, XI = (XB + 1023) / 1024;
+  static constexpr int XROW = KS * 2, XB = RB * XROW, XI = (XB + 1023) / 1024;  // (a row's pieces lie together)
   static constexpr int BYTES = WB + SB + XB;
   static constexpr int STEPS = SUB * KC / 32;  // products of 32 k
   static_assert(!I4 || SUB == 1, "one piece of a 4-bit row per stage");
-  static_assert(R == 8 || R % 16 == 0, "rows");
-  static_assert((GPC & (GPC - 1)) == 0 && (PR & (PR - 1)) == 0, "powers of two");
+  static_assert(R % 8 == 0 && (!DUAL || R % 16 == 0), "rows");
 
   // LDS rows of weights are 128 bytes, 16-byte piece c of row r at c ^ (r & 6): the
   // 16 lanes that a ds_read_b128 serves at once then read from all banks.  The
@@ -78,7 +77,7 @@ struct Stage {
   }
 
   // Row of the activations that lane l's part of copy n belongs to.
-  static __device__ __forceinline__ int x_row(int n, int lane) { return ((n * 1024 + lane * 16) / XROW) % RB; }
+  static __device__ __forceinline__ int x_row(int n, int lane) { return (n * 1024 + lane * 16) / XROW; }
 
   // Copies of the stage at k0 into LDS at `slot`: the weights and their scales.
   // A piece of a row that lies past K, or a row past `rows`, is not read.
@@ -110,22 +109,25 @@ struct Stage {
     }
   }
 
-  // ... and the activations; xr[n] is the byte offset of row x_row(n, lane), or
-  // NOWHERE.  Zeros past K.
-  static __device__ __forceinline__ void copy_x(const Source& s, const uint32_t (&xr)[XI], int k0, uint32_t slot,
-                                                int lane) {
+  // ... and the first `rows` (1 .. RB) rows of the activations; xr[n] is the byte
+  // offset of row x_row(n, lane).  Zeros past K.  Returns the number of copies.
+  static __device__ __forceinline__ int copy_x(const Source& s, const uint32_t (&xr)[XI], int rows, int k0,
+                                               uint32_t slot, int lane) {
+    const int bytes = rows * XROW;
 #pragma unroll
     for (int n = 0; n < XI; ++n) {
-      const int byte = n * 1024 + lane * 16;
-      const int k = (byte / (RB * XROW)) * KC + x_piece((byte % XROW) / 16, x_row(n, lane)) * 8;
-      const uint32_t v = k0 + k >= s.K ? NOWHERE : xr[n] + (uint32_t)k * 2;
-      if (XB % 1024 == 0 || byte < XB)
-        dma16(s.x, v, (uint32_t)k0 * 2, __builtin_amdgcn_readfirstlane(slot + WB + SB + n * 1024));
+      if (n * 1024 < bytes) {  // (uniform)
+        const int byte = n * 1024 + lane * 16, row = x_row(n, lane), in = byte - row * XROW;
+        const int k = (in / (KC * 2)) * KC + x_piece((in % (KC * 2)) / 16, row) * 8;
+        const uint32_t v = k0 + k >= s.K ? NOWHERE : xr[n] + (uint32_t)k * 2;
+        if (byte < bytes) dma16(s.x, v, (uint32_t)k0 * 2, __builtin_amdgcn_readfirstlane(slot + WB + SB + n * 1024));
+      }
     }
+    return (bytes + 1023) / 1024;
   }
 
   // A stage in registers, and its products added to acc (rows 16 t + 4 (l / 16)
-  // .. + 3, column l % 16; columns from RB on repeat others).
+  // .. + 3, column l % 16; columns without a row hold anything).
   bf16x8 b[STEPS];
   u32x4_t a[I4 ? 1 : STEPS][I4 ? 1 : RT];
   uint32_t c[I4 ? RT : 1][8];
@@ -134,7 +136,7 @@ struct Stage {
   __device__ __forceinline__ void read(const uint8_t* slot, int lane) {
     const int r = lane & 15, q = lane >> 4, col = r % RB;
     auto xb = [&](int sub, int piece) {
-      return *reinterpret_cast<const bf16x8*>(slot + WB + SB + (sub * RB + col) * XROW + x_pos(piece, col) * 16);
+      return *reinterpret_cast<const bf16x8*>(slot + WB + SB + col * XROW + sub * (KC * 2) + x_pos(piece, col) * 16);
     };
     if constexpr (!I4) {
 #pragma unroll
@@ -143,7 +145,7 @@ struct Stage {
         b[st] = xb(sub, 4 * ks + q);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          const int row = R == 8 ? r & 7 : 16 * t + r;
+          const int row = 16 * t + (R - 16 * t < 16 ? r & 7 : r);  // (half a tile: its rows twice)
           a[st][t] = *reinterpret_cast<const u32x4_t*>(slot + (sub * R + row) * 128 + (((4 * ks + q) ^ (row & 6)) << 4));
         }
       }
@@ -153,7 +155,7 @@ struct Stage {
       for (int st = 0; st < 8; ++st) b[st] = xb(0, (st / NJ) * (4 * NJ) + q * NJ + st % NJ);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const int row = R == 8 ? r & 7 : 16 * t + r;
+        const int row = 16 * t + (R - 16 * t < 16 ? r & 7 : r);  // (half a tile: its rows twice)
         const uint8_t* w = slot + row * 128;
         auto at = [&](int word) { return w + (((word >> 2) ^ (row & 6)) << 4) + (word & 3) * 4; };
 #pragma unroll
@@ -169,7 +171,7 @@ struct Stage {
             c[t][g] = *reinterpret_cast<const uint32_t*>(at(4 * g + q));
           }
           const int part = DUAL ? q >> 1 : 0;
-          const int srow = DUAL ? 8 * t + 4 * (q & 1) : R == 8 ? 4 * (q & 1) : 16 * t + 4 * q;
+          const int srow = DUAL ? 8 * t + 4 * (q & 1) : 16 * t + 4 * (R - 16 * t < 16 ? q & 1 : q);
           sc[g][t] = *reinterpret_cast<const f32x4_t*>(slot + WB + part * SIP * 256 + (g * PR + srow) * 4);
         }
       }
@@ -192,22 +194,61 @@ struct Stage {
     } else {
       constexpr int NJ = GRP / 32;
       const bf16x8 off = __builtin_bit_cast(bf16x8, u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
+      // (a few independent chains side by side: a product's result is not ready for the next one's start)
+      constexpr int GB = GPC < 4 ? GPC : RT > 1 ? 2 : 4;
 #pragma unroll
-      for (int g = 0; g < GPC; ++g) {
-        f32x4_t base = {0.f, 0.f, 0.f, 0.f};
+      for (int g0 = 0; g0 < GPC; g0 += GB) {
+        f32x4_t base[GB], p[GB][RT];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) base = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, b[g * NJ + j], base, 0, 0, 0);
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          f32x4_t p = base;
+          for (int g = 0; g < GB; ++g)
+            base[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, b[(g0 + g) * NJ + j],
+                                                              j ? base[g] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes(c[t][g * NJ + j]), b[g * NJ + j], p, 0, 0, 0);
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] += sc[g][t][i] * p[i];
-        }
+          for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int g = 0; g < GB; ++g)
+              p[g][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes(c[t][(g0 + g) * NJ + j]), b[(g0 + g) * NJ + j],
+                                                                j ? p[g][t] : base[g], 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < GB; ++g)
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] += sc[g0 + g][t][i] * p[g][t][i];
       }
     }
+  }
+};
+
+// Waits until at most n copies (of those last asked for) are outstanding, or
+// fewer: at once for n = COMMON, else for the next lower count that is coded.
+template <int COMMON>
+__device__ __forceinline__ void wait_younger(int n) {
+  if (n == COMMON) wait_vm<COMMON>();
+  else if (n >= 16) n >= 32 ? wait_vm<32>() : n >= 24 ? wait_vm<24>() : n >= 20 ? wait_vm<20>() : wait_vm<16>();
+  else if (n >= 8) n >= 12 ? wait_vm<12>() : n >= 10 ? wait_vm<10>() : wait_vm<8>();
+  else if (n >= 4) n >= 6 ? wait_vm<6>() : n >= 5 ? wait_vm<5>() : wait_vm<4>();
+  else n >= 3 ? wait_vm<3>() : n >= 2 ? wait_vm<2>() : n >= 1 ? wait_vm<1>() : wait_vm<0>();
+  asm volatile("" ::: "memory");
+}
+
+// Copies per stage of a ring, the oldest first, to know how many are younger than it.
+struct Ages {
+  uint64_t q = 0;
+  int n = 0, sum = 0;
+  __device__ __forceinline__ void push(int copies) {
+    q |= (uint64_t)(uint32_t)copies << (8 * n);
+    ++n;
+    sum += copies;
+  }
+  __device__ __forceinline__ void pop() {  // sum is then of the younger ones
+    sum -= (int)(q & 255);
+    q >>= 8;
+    --n;
   }
 };
 
