@@ -37,7 +37,9 @@ namespace {
 using dma::lds_barrier;
 
 constexpr int MAX_T = MOE_DECODE_MAX_T, MAX_K = 32, MAX_E = 1024;
-constexpr int SYNC_FLAGS = 64;  // sync[0]: the counter of workgroups; sync[SYNC_FLAGS + i]: number i's phase 1 is done
+// sync[0]: the counter of workgroups; sync[SYNC_TOKENS + t]: token t's selection is
+// there; sync[SYNC_FLAGS + i]: number i's phase 1 is done.
+constexpr int SYNC_TOKENS = 64, SYNC_FLAGS = SYNC_TOKENS + MAX_T;
 
 // ---------------------------------------------------------------------------
 // Router logits
@@ -123,83 +125,91 @@ struct alignas(8) Block {
   uint8_t off, nb; // which of the expert's blocks it is, and of how many
 };
 
-// Largest of the wave's values (none below 0), by moves along and across the rows of 16 lanes.
-template <int CTRL, int ROWS>
+// The largest of v over each aligned group of L lanes (a power of two), in all of them.
+template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ uint32_t wave_max_dpp(uint32_t v) {
-  v = dpp_max<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8: lane 15 of a row has the row's
-  v = dpp_max<0x112, 0xf>(v);
-  v = dpp_max<0x114, 0xf>(v);
-  v = dpp_max<0x118, 0xf>(v);
-  v = dpp_max<0x142, 0xa>(v);  // row_bcast:15, :31: lane 63 has the wave's
-  v = dpp_max<0x143, 0xc>(v);
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
+  if (L >= 2) v = dpp_max<0xB1>(v);    // quad_perm:[1,0,3,2]
+  if (L >= 4) v = dpp_max<0x4E>(v);    // quad_perm:[2,3,0,1]
+  if (L >= 8) v = dpp_max<0x141>(v);   // row_half_mirror
+  if (L >= 16) v = dpp_max<0x140>(v);  // row_mirror
+  if (L >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(s[0], s[1]);
+  }
+  if (L >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(s[0], s[1]);
+  }
+  return v;
 }
 
 // The selection of token t by one wave, as moe_route and moe_route_grouped
-// define it, to idx and w ([k], LDS).  keys: the wave's E words of LDS.  Per group
-// of experts its best k / n_groups one after the other: lane l keeps the best of
-// the group's experts l, l + 64, ...; the wave's best is found over the lanes, and
+// define it, to idx and w ([k], LDS).  keys: the wave's E words of LDS; pick: 2 k
+// words.  A group of experts belongs to L lanes, which hold its experts l, l + L,
+// ..; every group's best k / n_groups are taken one after the other, the groups
+// side by side: a lane knows its best, the group's is found over the lanes, and
 // its lane looks through its experts again.  Short code rather than few steps: it
-// runs once per launch, from a cold instruction cache (with a token's logits in
-// registers, unrolled for up to 16 a lane, the kernel was 128 KB long, and 12
-// tokens in 4 groups took 20 us; so, 4).
-__device__ __forceinline__ void route_token(const DecodeParams& p, int t, int lane, uint32_t* keys, int32_t* idx,
-                                            float* w) {
-  for (int e = lane; e < p.E; e += 64) {
-    float v = p.bias ? p.bias[e] : 0.f;
-    const float* row = p.part + (int64_t)t * p.E + e;
-    if (p.ks == 1) v += row[0];
-    else {
-      const int64_t ld = (int64_t)p.T * p.E;
-      v += (row[0] + row[ld]) + (row[2 * ld] + row[3 * ld]);
+// runs once per launch, from a cold instruction cache (unrolled, with a token's
+// logits in registers, the kernel was 128 KB long, and 12 tokens in 4 groups took
+// 20 us).
+__device__ __forceinline__ void route_token(const DecodeParams& p, int t, int lane, uint32_t* keys, uint32_t* pick,
+                                            int32_t* idx, float* w) {
+  // (the loads of four experts a lane together: one after the other they took 1.5 us each)
+  for (int e0 = lane; e0 < p.E; e0 += 256) {
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = min(e0 + 64 * u, p.E - 1);
+      const float* row = p.part + (int64_t)t * p.E + e;
+      const int64_t ld = p.ks == 1 ? 0 : (int64_t)p.T * p.E;
+      const float b = p.bias ? p.bias[e] : 0.f;
+      v[u] = p.ks == 1 ? b + row[0] : b + ((row[0] + row[ld]) + (row[2 * ld] + row[3 * ld]));
     }
-    keys[e] = max(order_key(v), 1u);  // 0: taken
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e0 + 64 * u < p.E) keys[e0 + 64 * u] = max(order_key(v[u]), 1u);  // 0: taken
   }
   const int Eg = p.E / p.n_groups, kg = p.k / p.n_groups;
-  uint32_t my_key = 0, my_i = 0;  // lane j: pick j
-  for (int g = 0, j = 0; g < p.n_groups; ++g) {
-    const uint32_t* kg_p = keys + g * Eg;
-    uint32_t best = 0, at = 0;
-    auto look = [&]() {
-      best = 0;
-      for (int e = lane; e < Eg; e += 64) {
-        const uint32_t v = kg_p[e];
-        if (v > best) best = v, at = e;
-      }
-    };
-    look();
-    for (int r = 0; r < kg; ++r, ++j) {
-      const uint32_t top = wave_max_dpp(best);
-      const uint32_t e = ~wave_max_dpp(best == top ? ~at : 0u);  // the lowest of equals
-      if (lane == j) my_key = top, my_i = g * Eg + e;
-      if (lane == (int)(e & 63)) {
-        keys[g * Eg + e] = 0;
-        look();
-      }
+  const int L = p.n_groups == 1 ? 64 : 64 >> (32 - __builtin_clz(p.n_groups - 1));
+  const int g = lane / L, l = lane % L;
+  const bool has = g < p.n_groups;
+  uint32_t best = 0, at = 0;
+  auto look = [&]() {
+    best = 0;
+    for (int e = l; e < Eg; e += L) {
+      const uint32_t v = keys[g * Eg + e];
+      if (v > best) best = v, at = e;
+    }
+  };
+  if (has) look();
+  for (int r = 0; r < kg; ++r) {
+    const uint32_t top = lanes_max(best, L);
+    const uint32_t e = ~lanes_max(best == top ? ~at : 0u, L);  // the lowest of equals
+    if (has && best == top && at == e) {
+      pick[g * kg + r] = top;
+      pick[p.k + g * kg + r] = g * Eg + e;
+      keys[g * Eg + e] = 0;
+      look();
     }
   }
+  __builtin_amdgcn_wave_barrier();
+  const uint32_t my_key = lane < p.k ? pick[lane] : 0, my_i = lane < p.k ? pick[p.k + lane] : 0;
   // Slots in falling order: pick j's is the number of picks before it.
   int rank = 0;
-  uint32_t first = 0;
   for (int j = 0; j < p.k; ++j) {
     const uint32_t kj = (uint32_t)__builtin_amdgcn_readlane((int)my_key, j);
     const uint32_t ij = (uint32_t)__builtin_amdgcn_readlane((int)my_i, j);
     rank += kj > my_key || (kj == my_key && ij < my_i);
-    first = max(first, kj);
   }
-  const float v0 = key_float(first);
-  float sum = 0.f;
-  const float ex = expf(key_float(my_key) - v0);
-  if (p.renorm) {
-    sum = lane < p.k ? ex : 0.f;
-  } else {
-    if (lane < p.k) keys[my_i] = my_key;
-    __builtin_amdgcn_wave_barrier();
-    for (int e = lane; e < p.E; e += 64) sum += expf(key_float(keys[e]) - v0);
-  }
+  const float v0 = key_float(lanes_max(my_key, 64));
+  const float ex = lane < p.k ? expf(key_float(my_key) - v0) : 0.f;
+  float sum = ex;
+  if (!p.renorm)
+    for (int e = lane; e < p.E; e += 64)
+      if (keys[e]) sum += expf(key_float(keys[e]) - v0);
   sum = wave_sum(sum);
   if (lane < p.k) {
     idx[rank] = (int)my_i;
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   constexpr int ROWS = TMAX * MAX_K, BLOCKS = TMAX <= RB ? (ROWS < MAX_E ? ROWS : MAX_E) : MAX_E + ROWS / RB;
   // Scratch of the selection, over the ring before it starts.
   constexpr int O_IDX = 0, O_W = O_IDX + ROWS * 4, O_MASK = O_W + ROWS * 4, O_BASE = O_MASK + MAX_E * 8,
-                O_KEY = O_BASE + MAX_E * 2, SCRATCH = O_KEY + (W + 1) * MAX_E * 4;
+                O_KEY = O_BASE + MAX_E * 2, KEYS = MAX_E + 2 * MAX_K, SCRATCH = O_KEY + (W + 1) * KEYS * 4;
   static_assert(SCRATCH <= RING, "scratch");
   static_assert(S1 >= 2 && S2 >= 2, "stages");
   __shared__ __attribute__((aligned(1024))) uint8_t ring_m[RING];
@@ -233,6 +243,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   __shared__ uint16_t s_row[ROWS];  // slots of the rows, by expert
   __shared__ uint16_t s_more[256];  // numbers taken over
   __shared__ int s_vid, s_nblk, s_cmd;
+  __shared__ uint64_t s_todo;
 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -247,15 +258,53 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   if (tid == 64 * W) number = (int)__hip_atomic_fetch_add(p.sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   for (int i = tid; i < p.NL; i += NT) l_mask[i] = 0;
   if (p.part) {
-    uint32_t* keys = reinterpret_cast<uint32_t*>(ring_m + O_KEY) + wave * MAX_E;
+    // Up to a token a wave: every workgroup selects for all.  More: one workgroup
+    // each, and the others wait for its flag, but not for long: if it has not
+    // started, they select for themselves.
+    uint32_t* keys = reinterpret_cast<uint32_t*>(ring_m + O_KEY) + wave * KEYS;
+    const bool shared = p.T > W + 1;
+    uint64_t todo = ~0ull >> (64 - p.T);  // tokens to select for here
+    if (shared) {
+      for (int t = blockIdx.x; t < p.T; t += G) {
+        if (wave == 0) {
+          route_token(p, t, lane, keys, keys + MAX_E, l_idx + t * p.k, l_w + t * p.k);
+          __builtin_amdgcn_wave_barrier();
+          if (lane < p.k) {
+            __hip_atomic_store(p.idx + t * p.k + lane, l_idx[t * p.k + lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(p.w + t * p.k + lane, l_w[t * p.k + lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          if (lane == 0)
+            __hip_atomic_store(p.sync + SYNC_TOKENS + t, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+      if (wave == 0) {
+        const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
+        for (;;) {
+          const bool there = lane >= p.T || __hip_atomic_load(p.sync + SYNC_TOKENS + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          todo = ~__ballot(there);
+          if (todo == 0 || __builtin_amdgcn_s_memrealtime() - t0 > 3000) break;  // 30 us
+          __builtin_amdgcn_s_sleep(1);
+        }
+        if (lane == 0) s_todo = todo;
+      }
+      __syncthreads();
+      todo = s_todo;
+      for (int i = tid; i < slots; i += NT)
+        if (!(todo >> (i / p.k) & 1)) {
+          l_idx[i] = __hip_atomic_load(p.idx + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          l_w[i] = __hip_atomic_load(p.w + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
 #pragma nounroll
-    for (int t = wave; t < p.T; t += W + 1) route_token(p, t, lane, keys, l_idx + t * p.k, l_w + t * p.k);
+    for (int t = wave; t < p.T; t += W + 1)
+      if (todo >> t & 1) route_token(p, t, lane, keys, keys + MAX_E, l_idx + t * p.k, l_w + t * p.k);
   } else {
     for (int i = tid; i < slots; i += NT) l_idx[i] = p.idx[i], l_w[i] = p.w[i];
   }
   if (tid == 64 * W) s_vid = number;
   __syncthreads();
-  if (p.part && blockIdx.x == 0)
+  if (p.part && p.T <= W + 1 && blockIdx.x == 0)
     for (int i = tid; i < slots; i += NT) p.idx[i] = l_idx[i], p.w[i] = l_w[i];
   const int vid = __builtin_amdgcn_readfirstlane(s_vid);
   if (vid >= G) return;  // (another workgroup has done this one's items)
@@ -499,7 +548,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
           wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
           ST1 s;
           s.read(ring_p + tail * ST1::BYTES, lane);
-          s.multiply(acc);
+          s.multiply(acc, ring_p + tail * ST1::BYTES, lane);
           reads_done();
           tail = tail + 1 == S1 ? 0 : tail + 1;
         }
@@ -599,7 +648,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
           wait_younger<(S2 - 1) * (PRE2 + 1)>(ages.sum);
           ST2 s;
           s.read(ring_p + tail * ST2::BYTES, lane);
-          s.multiply(acc);
+          s.multiply(acc, ring_p + tail * ST2::BYTES, lane);
           reads_done();
           tail = tail + 1 == S2 ? 0 : tail + 1;
         }

@@ -34,7 +34,26 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
+// dma16 of bytes that are read once: they are the first to leave the L2, which
+// keeps what is shared (activations, code).
+__device__ __forceinline__ void dma16_once(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile(
+      "s_nop 4\n\t"  // as in dma16
+      "buffer_load_dwordx4 %0, %1, %2 offen nt lds"
+      :
+      : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds)
+      : "memory");
+}
+
 constexpr uint32_t NOWHERE = 0x80000000u;  // an offset past every resource: the copy writes zeros
+
+// The same resource in scalar registers (it is wave-uniform; kept across a loop
+// it may have become a vector value, which a copy's operand cannot be).
+__device__ __forceinline__ i32x4 scalar(i32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_readfirstlane(v[i]);
+  return v;
+}
 
 // What a stage's copies read: the weights' rows (DUAL: of two matrices), their
 // scales, the activations.  Bases may differ from tile to tile, pitches are in bytes.
@@ -86,13 +105,15 @@ struct Stage {
     const int row_bytes = I4 ? (s.K / 2 + 15) & ~15 : s.K * 2;
     const int at = I4 ? k0 / 2 : k0 * 2;
     const bool tail = at + SUB * 128 > row_bytes;  // (uniform)
+    const i32x4 w[2] = {scalar(s.w[0]), DUAL ? scalar(s.w[1]) : i32x4{}};
+    const uint32_t soff = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
     for (int j = 0; j < WI; ++j) {
       const int sub = j / (R / 8), jr = j % (R / 8);
       const int part = DUAL ? jr & 1 : 0, row = (DUAL ? jr >> 1 : jr) * 8 + r8;
       uint32_t v = (uint32_t)row * s.pitch + (uint32_t)(sub * 128 + piece * 16);
       if (row >= s.rows || (tail && at + sub * 128 + piece * 16 >= row_bytes)) v = NOWHERE;
-      dma16(s.w[part], v, (uint32_t)at, __builtin_amdgcn_readfirstlane(slot + j * 1024));
+      dma16_once(w[part], v, soff, __builtin_amdgcn_readfirstlane(slot + j * 1024));
     }
     if constexpr (I4) {
       const int g0 = k0 / GRP, groups = (s.K + GRP - 1) / GRP;
@@ -103,7 +124,7 @@ struct Stage {
           const int i = n * 64 + lane, g = i / PR, row = i % PR;
           const uint32_t v = g >= GPC || g0 + g >= groups || row >= s.rows
                                  ? NOWHERE : (uint32_t)row * s.spitch + (uint32_t)g * 4;
-          touch4u(s.s[p], v, (uint32_t)(g0 * 4),
+          touch4u(scalar(s.s[p]), v, __builtin_amdgcn_readfirstlane(g0 * 4),
                   __builtin_amdgcn_readfirstlane(slot + WB + (p * SIP + n) * 256));
         }
     }
@@ -114,13 +135,15 @@ struct Stage {
   static __device__ __forceinline__ int copy_x(const Source& s, const uint32_t (&xr)[XI], int rows, int k0,
                                                uint32_t slot, int lane) {
     const int bytes = rows * XROW;
+    const i32x4 x = scalar(s.x);
+    const uint32_t soff = __builtin_amdgcn_readfirstlane(k0 * 2);
 #pragma unroll
     for (int n = 0; n < XI; ++n) {
       if (n * 1024 < bytes) {  // (uniform)
         const int byte = n * 1024 + lane * 16, row = x_row(n, lane), in = byte - row * XROW;
         const int k = (in / (KC * 2)) * KC + x_piece((in % (KC * 2)) / 16, row) * 8;
         const uint32_t v = k0 + k >= s.K ? NOWHERE : xr[n] + (uint32_t)k * 2;
-        if (byte < bytes) dma16(s.x, v, (uint32_t)k0 * 2, __builtin_amdgcn_readfirstlane(slot + WB + SB + n * 1024));
+        if (byte < bytes) dma16(x, v, soff, __builtin_amdgcn_readfirstlane(slot + WB + SB + n * 1024));
       }
     }
     return (bytes + 1023) / 1024;
@@ -131,7 +154,6 @@ struct Stage {
   bf16x8 b[STEPS];
   u32x4_t a[I4 ? 1 : STEPS][I4 ? 1 : RT];
   uint32_t c[I4 ? RT : 1][8];
-  f32x4_t sc[I4 ? GPC : 1][I4 ? RT : 1];
 
   __device__ __forceinline__ void read(const uint8_t* slot, int lane) {
     const int r = lane & 15, q = lane >> 4, col = r % RB;
@@ -170,9 +192,6 @@ struct Stage {
           } else {
             c[t][g] = *reinterpret_cast<const uint32_t*>(at(4 * g + q));
           }
-          const int part = DUAL ? q >> 1 : 0;
-          const int srow = DUAL ? 8 * t + 4 * (q & 1) : 16 * t + 4 * (R - 16 * t < 16 ? q & 1 : q);
-          sc[g][t] = *reinterpret_cast<const f32x4_t*>(slot + WB + part * SIP * 256 + (g * PR + srow) * 4);
         }
       }
     }
@@ -184,7 +203,7 @@ struct Stage {
     return __builtin_bit_cast(bf16x8, v);
   }
 
-  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RT]) const {
+  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RT], const uint8_t* slot, int lane) const {
     if constexpr (!I4) {
 #pragma unroll
       for (int st = 0; st < STEPS; ++st)
@@ -216,9 +235,14 @@ struct Stage {
 #pragma unroll
         for (int g = 0; g < GB; ++g)
 #pragma unroll
-          for (int t = 0; t < RT; ++t)
+          for (int t = 0; t < RT; ++t) {
+            const int q = lane >> 4, part = DUAL ? q >> 1 : 0;
+            const int row = DUAL ? 8 * t + 4 * (q & 1) : 16 * t + 4 * (R - 16 * t < 16 ? q & 1 : q);
+            const f32x4_t sc =
+                *reinterpret_cast<const f32x4_t*>(slot + WB + part * SIP * 256 + ((g0 + g) * PR + row) * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] += sc[g0 + g][t][i] * p[g][t][i];
+            for (int i = 0; i < 4; ++i) acc[t][i] += sc[i] * p[g][t][i];
+          }
       }
     }
   }
