@@ -723,7 +723,8 @@ hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
     constexpr int SMALL = GRP == 32 ? 14592 : 17408;
     if (p.T <= 2) return wide ? run<GRP, 2, 2, 16, 24, 1, 8, SMALL>(p, grid, s) : run<GRP, 2, 2, 16, 8, 1, 8, SMALL>(p, grid, s);
     if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8, 16384>(p, grid, s);
-    return wide ? run<GRP, MAX_T, 8, 32, 24, 1, 4, 28672>(p, grid, s) : run<GRP, MAX_T, 8, 32, 8, 1, 4, 28672>(p, grid, s);
+    constexpr int RB = GRP == 128 ? 4 : 3;
+    return wide ? run<GRP, MAX_T, RB, 16, 24, 1, 8, 10752>(p, grid, s) : run<GRP, MAX_T, RB, 16, 8, 1, 8, 10752>(p, grid, s);
   }
 }
 

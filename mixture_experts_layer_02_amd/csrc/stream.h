@@ -100,34 +100,39 @@ struct Stage {
 
   // Copies of the stage at k0 into LDS at `slot`: the weights and their scales.
   // A piece of a row that lies past K, or a row past `rows`, is not read.
-  static __device__ __forceinline__ void copy_w(const Source& s, int k0, uint32_t slot, int lane) {
-    const int r8 = lane >> 3, piece = (lane & 7) ^ (r8 & 6);
-    const int row_bytes = I4 ? (s.K / 2 + 15) & ~15 : s.K * 2;
-    const int at = I4 ? k0 / 2 : k0 * 2;
-    const bool tail = at + SUB * 128 > row_bytes;  // (uniform)
+  template <bool EDGE>
+  static __device__ __forceinline__ void copy_w_as(const Source& s, int k0, uint32_t slot, int lane) {
+    const int r8 = lane >> 3, piece = ((lane & 7) ^ (r8 & 6)) * 16;
+    const int at = I4 ? k0 / 2 : k0 * 2, left = (I4 ? (s.K / 2 + 15) & ~15 : s.K * 2) - at;  // bytes of the row from at on
     const i32x4 w[2] = {scalar(s.w[0]), DUAL ? scalar(s.w[1]) : i32x4{}};
     const uint32_t soff = __builtin_amdgcn_readfirstlane(at);
+    const uint32_t v0 = __umul24(r8, s.pitch) + piece;  // (pitch < 2^24)
 #pragma unroll
     for (int j = 0; j < WI; ++j) {
       const int sub = j / (R / 8), jr = j % (R / 8);
-      const int part = DUAL ? jr & 1 : 0, row = (DUAL ? jr >> 1 : jr) * 8 + r8;
-      uint32_t v = (uint32_t)row * s.pitch + (uint32_t)(sub * 128 + piece * 16);
-      if (row >= s.rows || (tail && at + sub * 128 + piece * 16 >= row_bytes)) v = NOWHERE;
+      const int part = DUAL ? jr & 1 : 0, row = (DUAL ? jr >> 1 : jr) * 8;
+      uint32_t v = v0 + (uint32_t)row * s.pitch + (uint32_t)(sub * 128);
+      if (EDGE) v = (int)(row + r8 >= s.rows) | (int)(sub * 128 + piece >= left) ? NOWHERE : v;
       dma16_once(w[part], v, soff, __builtin_amdgcn_readfirstlane(slot + j * 1024));
     }
     if constexpr (I4) {
-      const int g0 = k0 / GRP, groups = (s.K + GRP - 1) / GRP;
+      const int g0 = k0 / GRP, groups = (s.K + GRP - 1) / GRP - g0;  // (from g0 on)
+      const uint32_t sat = __builtin_amdgcn_readfirstlane(g0 * 4);
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p)
+      for (int n = 0; n < SIP; ++n) {
+        const int i = n * 64 + lane, g = i / PR, row = i - g * PR;
+        uint32_t v = __umul24(row, s.spitch) + (uint32_t)g * 4;
+        if (EDGE) v = (int)(g >= groups) | (int)(row >= s.rows) ? NOWHERE : v;
+        if (GPC * PR % 64 && n == SIP - 1) v = g >= GPC ? NOWHERE : v;
 #pragma unroll
-        for (int n = 0; n < SIP; ++n) {
-          const int i = n * 64 + lane, g = i / PR, row = i % PR;
-          const uint32_t v = g >= GPC || g0 + g >= groups || row >= s.rows
-                                 ? NOWHERE : (uint32_t)row * s.spitch + (uint32_t)g * 4;
-          touch4u(scalar(s.s[p]), v, __builtin_amdgcn_readfirstlane(g0 * 4),
-                  __builtin_amdgcn_readfirstlane(slot + WB + (p * SIP + n) * 256));
-        }
+        for (int p = 0; p < PARTS; ++p)
+          touch4u(scalar(s.s[p]), v, sat, __builtin_amdgcn_readfirstlane(slot + WB + (p * SIP + n) * 256));
+      }
     }
+  }
+  static __device__ __forceinline__ void copy_w(const Source& s, int k0, uint32_t slot, int lane) {
+    if (k0 + KS > s.K || s.rows < PR) copy_w_as<true>(s, k0, slot, lane);
+    else copy_w_as<false>(s, k0, slot, lane);
   }
 
   // ... and the first `rows` (1 .. RB) rows of the activations; xr[n] is the byte
@@ -197,9 +202,10 @@ struct Stage {
     }
   }
 
-  static __device__ __forceinline__ bf16x8 codes(uint32_t w) {
-    constexpr uint32_t M = 0x00780078u, O = 0x41804180u;
-    const u32x4_t v = {((w << 3) & M) | O, ((w >> 1) & M) | O, ((w >> 5) & M) | O, ((w >> 9) & M) | O};
+  // (mask and base are held in registers, so that each pair takes a shift and one bit-field insert)
+  static __device__ __forceinline__ bf16x8 codes(uint32_t w, uint32_t mask, uint32_t base) {
+    auto put = [&](uint32_t v) { return (v & mask) | (base & ~mask); };
+    const u32x4_t v = {put(w << 3), put(w >> 1), put(w >> 5), put(w >> 9)};
     return __builtin_bit_cast(bf16x8, v);
   }
 
@@ -212,6 +218,8 @@ struct Stage {
           acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[st][t]), b[st], acc[t], 0, 0, 0);
     } else {
       constexpr int NJ = GRP / 32;
+      uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+      asm("" : "+s"(mask), "+v"(sixteen));
       const bf16x8 off = __builtin_bit_cast(bf16x8, u32x4_t{0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u});  // -24
       // (a few independent chains side by side: a product's result is not ready for the next one's start)
       constexpr int GB = GPC < 4 ? GPC : RT > 1 ? 2 : 4;
@@ -230,7 +238,7 @@ struct Stage {
           for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int g = 0; g < GB; ++g)
-              p[g][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes(c[t][(g0 + g) * NJ + j]), b[(g0 + g) * NJ + j],
+              p[g][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes(c[t][(g0 + g) * NJ + j], mask, sixteen), b[(g0 + g) * NJ + j],
                                                                 j ? p[g][t] : base[g], 0, 0, 0);
 #pragma unroll
         for (int g = 0; g < GB; ++g)
