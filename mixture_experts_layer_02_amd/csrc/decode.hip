@@ -230,7 +230,9 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   constexpr int RP = R1 + 4;  // pitch of phase 1's partial sums (floats)
   constexpr int RED = 2 * W * RB * RP * 4, YACC = W * TMAX * R2 * 4, ACC = RED > YACC ? RED : YACC;
   constexpr int RING = W * RINGW, NT = 64 * (W + 1);
-  constexpr int ROWS = TMAX * MAX_K, BLOCKS = TMAX <= RB ? (ROWS < MAX_E ? ROWS : MAX_E) : MAX_E + ROWS / RB;
+  constexpr int ROWS = TMAX * MAX_K, EXPERTS = ROWS < MAX_E ? ROWS : MAX_E;
+  // (an expert of n rows has at most 1 + (n - 1) / RB blocks)
+  constexpr int BLOCKS = EXPERTS + (TMAX <= RB ? 0 : (ROWS - EXPERTS) / RB);
   // Scratch of the selection, over the ring before it starts.
   constexpr int O_IDX = 0, O_W = O_IDX + ROWS * 4, O_MASK = O_W + ROWS * 4, O_BASE = O_MASK + MAX_E * 8,
                 O_KEY = O_BASE + MAX_E * 2, KEYS = MAX_E + 2 * MAX_K, SCRATCH = O_KEY + (W + 1) * KEYS * 4;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t acc_m[ACC];
   __shared__ Block s_blk[BLOCKS];
   __shared__ float s_roww[ROWS];
-  __shared__ uint16_t s_row[ROWS];  // slots of the rows, by expert
+  __shared__ uint32_t s_row[ROWS];  // slots (low 16 bits) and tokens of the rows, by expert
   __shared__ uint16_t s_more[256];  // numbers taken over
   __shared__ int s_vid, s_nblk, s_cmd;
   __shared__ uint64_t s_todo;
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       }
     if (!first) continue;
     const int pos = l_base[e] + __popcll(l_mask[e] & ((1ull << t) - 1));
-    s_row[pos] = (uint16_t)i;
+    s_row[pos] = (uint32_t)i | (uint32_t)t << 16;
     s_roww[pos] = w;
   }
   __syncthreads();
@@ -365,15 +367,24 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     return __builtin_bit_cast(Block, u32x2_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)v[0]),
                                              (uint32_t)__builtin_amdgcn_readfirstlane((int)v[1])});
   };
-  // Phase-1 item i: a channel tile's blocks follow one another, then the next tile's.
-  auto item1 = [&](int i, Block& b, int& tile) {
-    const int bi = i / tiles1;
-    b = block(bi);
-    tile = i - bi * tiles1;
+  // Phase-1 items: block bi's share of the tiles; a channel tile's blocks follow one
+  // another, then the next tile's.  Moved on by G items with adds alone.
+  const int g_blk = G / tiles1, g_tile = G - g_blk * tiles1;
+  struct Item {
+    int i, bi, at;  // bi * tiles1 + at = i
+  };
+  auto first_item = [&](int i) { return Item{i, i / tiles1, i % tiles1}; };
+  auto next_item = [&](Item& m) {
+    m.i += G, m.bi += g_blk, m.at += g_tile;
+    if (m.at >= tiles1) m.at -= tiles1, ++m.bi;
+  };
+  auto item1 = [&](const Item& m, Block& b, int& tile) {
+    b = block(m.bi);
+    tile = m.at;
     if (TMAX > RB && b.nb > 1) {
-      const int b0 = bi - b.off, local = i - b0 * tiles1;
+      const int local = b.off * tiles1 + m.at;
       tile = local / b.nb;
-      b = block(b0 + local % b.nb);
+      b = block(m.bi - b.off + local % b.nb);
     }
   };
 
@@ -401,26 +412,27 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   if (wave == W) {  // ---- the serving wave
     bool take = true;
     for (int cur = vid;;) {
+      Item m = first_item(cur);
 #pragma nounroll
-      for (int item = cur, n = 0; item < n1; item += G, ++n) {
+      for (int n = 0; m.i < n1; next_item(m), ++n) {
         Block b;
         int tile;
-        item1(item, b, tile);
+        item1(m, b, tile);
         lds_barrier();  // the item's partial sums are in red[n % 2]
         const float* rd = red + (n & 1) * W * RB * RP;
-        for (int i = lane; i < b.n * (PR1 / 2); i += 64) {
-          const int row = i / (PR1 / 2), c = (i % (PR1 / 2)) * 2, at = row * RP + (c / 8) * 16 + c % 8;
-          float g[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
+        // Lane l: row l / 16 of four, row l % 16 (8 gate, 8 up) of a 16-row tile.
+        for (int i = 0; i < b.n * (R1 / 16); i += 4) {
+          const int j = i + q, row = j / (R1 / 16), t = j % (R1 / 16);
+          float v = 0.f;
+          if (row < b.n) {
 #pragma unroll
-          for (int w = 0; w < W; ++w)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              g[j] += rd[w * RB * RP + at + j];
-              u[j] += rd[w * RB * RP + at + 8 + j];
-            }
-          const uint32_t hv = pack_bf2(g[0] * sigmoidf_(g[0]) * u[0], g[1] * sigmoidf_(g[1]) * u[1]);
-          __hip_atomic_store(reinterpret_cast<uint32_t*>(p.h + (int64_t)s_row[b.pos + row] * p.f + tile * PR1 + c), hv,
-                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            for (int w = 0; w < W; ++w) v += rd[(w * RB + row) * RP + 16 * t + r];
+          }
+          const float up = __shfl_xor(v, 8, WAVE), hv = v * sigmoidf_(v) * up, other = __shfl_xor(hv, 1, WAVE);
+          if (row < b.n && r < 8 && r % 2 == 0)
+            __hip_atomic_store(reinterpret_cast<uint32_t*>(p.h + (int64_t)(s_row[b.pos + row] & 0xffff) * p.f + tile * PR1 +
+                                                           8 * t + r),
+                               pack_bf2(hv, other), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
       }
       // h was stored past the XCD's L2 (atomic, at agent scope), so its stores being
@@ -479,6 +491,15 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   }
 
   // ---- a streaming wave
+  // (What only the start of an item needs is read from the arguments there, not
+  // kept in scalar registers, of which the loops have too few: spilled ones cost
+  // a vector instruction each time.)
+  typedef const __attribute__((address_space(4))) DecodeParams* Args;
+  auto args = [&]() {
+    Args a = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return a;
+  };
   const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring_m) + wave * RINGW;
   const uint8_t* ring_p = ring_m + wave * RINGW;
   Ages ages;
@@ -491,23 +512,25 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   uint32_t xr2[ST2::XI];
   int rows2 = 0;
   auto source2 = [&](int item, int blk) {
-    const int64_t pitch = GRP ? p.f / 2 : (int64_t)p.f * 2;
+    const Args a = args();
+    const int d = a->d, f = a->f;
+    const int64_t pitch = GRP ? f / 2 : (int64_t)f * 2;
     const Block b = block(blk);
-    const int64_t row = (int64_t)b.e * p.d + item * R2;
-    src.rows = min(R2, p.d - item * R2);
-    src.w[0] = make_rsrc(p.w2 + row * pitch, src.rows * pitch);
+    const int64_t row = (int64_t)b.e * d + item * R2;
+    src.rows = min(R2, d - item * R2);
+    src.w[0] = make_rsrc(a->w2 + row * pitch, src.rows * pitch);
     src.pitch = (uint32_t)pitch;
     if (GRP) {
-      const int groups = (p.f + GRP - 1) / (GRP ? GRP : 1);
-      src.s[0] = make_rsrc(p.s2 + row * groups, (uint64_t)src.rows * groups * 4);
+      const int groups = (f + GRP - 1) / (GRP ? GRP : 1);
+      src.s[0] = make_rsrc(a->s2 + row * groups, (uint64_t)src.rows * groups * 4);
       src.spitch = groups * 4;
     }
-    src.x = make_rsrc(p.h, (uint64_t)slots * p.f * 2);
-    src.K = p.f;
+    src.x = make_rsrc(a->h, (uint64_t)(a->T * a->k) * f * 2);
+    src.K = f;
     rows2 = b.n;
 #pragma unroll
     for (int n = 0; n < ST2::XI; ++n)
-      xr2[n] = (uint32_t)s_row[b.pos + min(ST2::x_row(n, lane), b.n - 1)] * (uint32_t)p.f * 2;
+      xr2[n] = (s_row[b.pos + min(ST2::x_row(n, lane), b.n - 1)] & 0xffff) * (uint32_t)f * 2;
   };
   // The stage to copy next in phase 2.
   int c_item = vid, c_blk = blk2, c_st = st2, c_left = per2;
@@ -532,7 +555,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       }
     } else {
       uint32_t xr1[ST1::XI];
-      int rows1 = 0, c_at = 0, c_i = cur;     // copied next: stage of the item, item
+      int rows1 = 0, c_at = 0;  // copied next: stage of the item, item
+      Item c_m = first_item(cur);
       int u_at = 0, u_n = 0, head = 0, tail = 0;  // used next: stage of the item, item's place; ring slots
       f32x4_t acc[ST1::RT];
 #pragma unroll
@@ -542,7 +566,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       src.x = make_rsrc(p.x, (uint64_t)p.T * p.d * 2);
 #pragma nounroll
       while (u_n < items) {
-        const bool copies = c_i < n1, use = ages.n == S1 || !copies;
+        const bool copies = c_m.i < n1, use = ages.n == S1 || !copies;
         if (use) {
           ages.pop();
           wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
@@ -554,29 +578,31 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         }
         if (copies) {
           if (c_at == 0) {
+            const Args a = args();
+            const int d = a->d;
             Block b;
             int tile;
-            item1(c_i, b, tile);
-            const int64_t row = (int64_t)b.e * p.f + tile * PR1, pitch = GRP ? p.d / 2 : (int64_t)p.d * 2;
-            src.w[0] = make_rsrc(p.w1 + row * pitch, PR1 * pitch);
-            src.w[1] = make_rsrc(p.w3 + row * pitch, PR1 * pitch);
+            item1(c_m, b, tile);
+            const int64_t row = (int64_t)b.e * a->f + tile * PR1, pitch = GRP ? d / 2 : (int64_t)d * 2;
+            src.w[0] = make_rsrc(a->w1 + row * pitch, PR1 * pitch);
+            src.w[1] = make_rsrc(a->w3 + row * pitch, PR1 * pitch);
             if (GRP) {
-              const int groups = (p.d + GRP - 1) / (GRP ? GRP : 1);
-              src.s[0] = make_rsrc(p.s1 + row * groups, (uint64_t)PR1 * groups * 4);
-              src.s[1] = make_rsrc(p.s3 + row * groups, (uint64_t)PR1 * groups * 4);
+              const int groups = (d + GRP - 1) / (GRP ? GRP : 1);
+              src.s[0] = make_rsrc(a->s1 + row * groups, (uint64_t)PR1 * groups * 4);
+              src.s[1] = make_rsrc(a->s3 + row * groups, (uint64_t)PR1 * groups * 4);
               src.spitch = groups * 4;
             }
             rows1 = b.n;
 #pragma unroll
             for (int n = 0; n < ST1::XI; ++n)
-              xr1[n] = (uint32_t)(s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] / p.k) * (uint32_t)p.d * 2;
+              xr1[n] = (s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] >> 16) * (uint32_t)d * 2;
           }
           const int k0 = (s0 + c_at) * ST1::KS;
           const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST1::BYTES);
           ST1::copy_w(src, k0, at, lane);
           ages.push(PRE1 + ST1::copy_x(src, xr1, rows1, k0, at, lane));
           head = head + 1 == S1 ? 0 : head + 1;
-          if (++c_at == per1) c_at = 0, c_i += G;
+          if (++c_at == per1) c_at = 0, next_item(c_m);
         }
         if (use) {
           if (++u_at == per1) {
@@ -667,9 +693,9 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
           if (++st == C2 || left == 0) {  // the block's products, times the routing weights, to their tokens
             const Block b = block(blk);
             if (r < b.n) {
-              const int slot = s_row[b.pos + r];
+              const int token = s_row[b.pos + r] >> 16;
               const float w = s_roww[b.pos + r];
-              float* to = mine + (slot / p.k) * R2 + 4 * q;
+              float* to = mine + token * R2 + 4 * q;
 #pragma unroll
               for (int t = 0; t < ST2::RT; ++t)
                 if (R2 - 16 * t >= 16 || q < 2) {
@@ -720,9 +746,11 @@ hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
     if (p.T <= 16) return wide ? run<0, 16, 16, 16, 24, 1, 8, 16384>(p, grid, s) : run<0, 16, 16, 16, 8, 2, 8, 16384>(p, grid, s);
     return wide ? run<0, MAX_T, 12, 16, 24, 1, 8, 10752>(p, grid, s) : run<0, MAX_T, 12, 16, 8, 2, 8, 10752>(p, grid, s);
   } else {
-    constexpr int SMALL = GRP == 32 ? 14592 : 17408;
-    if (p.T <= 2) return wide ? run<GRP, 2, 2, 16, 24, 1, 8, SMALL>(p, grid, s) : run<GRP, 2, 2, 16, 8, 1, 8, SMALL>(p, grid, s);
-    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8, 16384>(p, grid, s);
+    // (twelve waves where their registers hold a stage of the smaller groups' scales too)
+    constexpr int W2 = GRP == 32 ? 8 : 12, RING2 = GRP == 32 ? 14592 : 11264;
+    if (p.T <= 2) return wide ? run<GRP, 2, 2, 16, 24, 1, W2, RING2>(p, grid, s) : run<GRP, 2, 2, 16, 8, 1, W2, RING2>(p, grid, s);
+    constexpr int W16 = GRP == 128 ? 12 : 8, RING16 = GRP == 128 ? 10752 : 16384;
+    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, W16, RING16>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, W16, RING16>(p, grid, s);
     constexpr int RB = GRP == 128 ? 4 : 3;
     return wide ? run<GRP, MAX_T, RB, 16, 24, 1, 8, 10752>(p, grid, s) : run<GRP, MAX_T, RB, 16, 8, 1, 8, 10752>(p, grid, s);
   }
