@@ -564,59 +564,58 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       src.pitch = (uint32_t)(GRP ? p.d / 2 : p.d * 2);
       src.K = p.d, src.rows = PR1;
       src.x = make_rsrc(p.x, (uint64_t)p.T * p.d * 2);
+      auto copy = [&]() {
+                  if (c_at == 0) {
+                    const Args a = args();
+                    const int d = a->d;
+                    Block b;
+                    int tile;
+                    item1(c_m, b, tile);
+                    const int64_t row = (int64_t)b.e * a->f + tile * PR1, pitch = GRP ? d / 2 : (int64_t)d * 2;
+                    src.w[0] = make_rsrc(a->w1 + row * pitch, PR1 * pitch);
+                    src.w[1] = make_rsrc(a->w3 + row * pitch, PR1 * pitch);
+                    if (GRP) {
+                      const int groups = (d + GRP - 1) / (GRP ? GRP : 1);
+                      src.s[0] = make_rsrc(a->s1 + row * groups, (uint64_t)PR1 * groups * 4);
+                      src.s[1] = make_rsrc(a->s3 + row * groups, (uint64_t)PR1 * groups * 4);
+                      src.spitch = groups * 4;
+                    }
+                    rows1 = b.n;
+        #pragma unroll
+                    for (int n = 0; n < ST1::XI; ++n)
+                      xr1[n] = (s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] >> 16) * (uint32_t)d * 2;
+                  }
+                  const int k0 = (s0 + c_at) * ST1::KS;
+                  const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST1::BYTES);
+                  ST1::copy_w(src, k0, at, lane);
+                  ages.push(PRE1 + ST1::copy_x(src, xr1, rows1, k0, at, lane));
+                  head = head + 1 == S1 ? 0 : head + 1;
+                  if (++c_at == per1) c_at = 0, next_item(c_m);
+      };
+#pragma nounroll
+      while (ages.n < S1 && c_m.i < n1) copy();
 #pragma nounroll
       while (u_n < items) {
-        const bool copies = c_m.i < n1, use = ages.n == S1 || !copies;
-        if (use) {
-          ages.pop();
-          wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
-          ST1 s;
-          s.read(ring_p + tail * ST1::BYTES, lane);
-          s.multiply(acc, ring_p + tail * ST1::BYTES, lane);
-          reads_done();
-          tail = tail + 1 == S1 ? 0 : tail + 1;
-        }
-        if (copies) {
-          if (c_at == 0) {
-            const Args a = args();
-            const int d = a->d;
-            Block b;
-            int tile;
-            item1(c_m, b, tile);
-            const int64_t row = (int64_t)b.e * a->f + tile * PR1, pitch = GRP ? d / 2 : (int64_t)d * 2;
-            src.w[0] = make_rsrc(a->w1 + row * pitch, PR1 * pitch);
-            src.w[1] = make_rsrc(a->w3 + row * pitch, PR1 * pitch);
-            if (GRP) {
-              const int groups = (d + GRP - 1) / (GRP ? GRP : 1);
-              src.s[0] = make_rsrc(a->s1 + row * groups, (uint64_t)PR1 * groups * 4);
-              src.s[1] = make_rsrc(a->s3 + row * groups, (uint64_t)PR1 * groups * 4);
-              src.spitch = groups * 4;
-            }
-            rows1 = b.n;
+        ages.pop();
+        wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
+        ST1 s;
+        s.read(ring_p + tail * ST1::BYTES, lane);
+        if (!ST1::EARLY) s.multiply(acc, lane);
+        reads_done();
+        tail = tail + 1 == S1 ? 0 : tail + 1;
+        if (c_m.i < n1) copy();
+        if (ST1::EARLY) s.multiply(acc, lane);
+        if (++u_at == per1) {
+          float* rd = red + ((u_n & 1) * W + wave) * RB * RP;
+          if (r < RB) {
 #pragma unroll
-            for (int n = 0; n < ST1::XI; ++n)
-              xr1[n] = (s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] >> 16) * (uint32_t)d * 2;
+            for (int t = 0; t < ST1::RT; ++t) *reinterpret_cast<f32x4_t*>(rd + r * RP + 16 * t + 4 * q) = acc[t];
           }
-          const int k0 = (s0 + c_at) * ST1::KS;
-          const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST1::BYTES);
-          ST1::copy_w(src, k0, at, lane);
-          ages.push(PRE1 + ST1::copy_x(src, xr1, rows1, k0, at, lane));
-          head = head + 1 == S1 ? 0 : head + 1;
-          if (++c_at == per1) c_at = 0, next_item(c_m);
-        }
-        if (use) {
-          if (++u_at == per1) {
-            float* rd = red + ((u_n & 1) * W + wave) * RB * RP;
-            if (r < RB) {
 #pragma unroll
-              for (int t = 0; t < ST1::RT; ++t) *reinterpret_cast<f32x4_t*>(rd + r * RP + 16 * t + 4 * q) = acc[t];
-            }
-#pragma unroll
-            for (int t = 0; t < ST1::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            u_at = 0;
-            ++u_n;
-            lds_barrier();
-          }
+          for (int t = 0; t < ST1::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          u_at = 0;
+          ++u_n;
+          lds_barrier();
         }
       }
     }
@@ -659,6 +658,18 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     const int items = count(first, n2);
     int copies = items * per2 - ages.n;  // stages that are still to be copied
     float* mine = yacc + wave * p.T * R2;
+    auto copy = [&]() {
+      if (c_new) source2(c_item, c_blk);
+      const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST2::BYTES);
+      const int k0 = c_st * ST2::KS;
+      ST2::copy_w(src, k0, at, lane);
+      ages.push(PRE2 + ST2::copy_x(src, xr2, rows2, k0, at, lane));
+      next2();
+      head = head + 1 == S2 ? 0 : head + 1;
+      --copies;
+    };
+#pragma nounroll
+    while (ages.n < S2 && copies > 0) copy();
 #pragma nounroll
     for (int n = 0; n < items; ++n) {
       for (int i = lane; i < p.T * R2; i += 64) mine[i] = 0.f;
@@ -668,48 +679,35 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       int blk = blk2, st = st2;
 #pragma nounroll
       for (int left = per2; left > 0;) {
-        const bool use = ages.n == S2 || copies == 0;
-        if (use) {
-          ages.pop();
-          wait_younger<(S2 - 1) * (PRE2 + 1)>(ages.sum);
-          ST2 s;
-          s.read(ring_p + tail * ST2::BYTES, lane);
-          s.multiply(acc, ring_p + tail * ST2::BYTES, lane);
-          reads_done();
-          tail = tail + 1 == S2 ? 0 : tail + 1;
-        }
-        if (copies > 0) {
-          if (c_new) source2(c_item, c_blk);
-          const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST2::BYTES);
-          const int k0 = c_st * ST2::KS;
-          ST2::copy_w(src, k0, at, lane);
-          ages.push(PRE2 + ST2::copy_x(src, xr2, rows2, k0, at, lane));
-          next2();
-          head = head + 1 == S2 ? 0 : head + 1;
-          --copies;
-        }
-        if (use) {
-          --left;
-          if (++st == C2 || left == 0) {  // the block's products, times the routing weights, to their tokens
-            const Block b = block(blk);
-            if (r < b.n) {
-              const int token = s_row[b.pos + r] >> 16;
-              const float w = s_roww[b.pos + r];
-              float* to = mine + token * R2 + 4 * q;
+        ages.pop();
+        wait_younger<(S2 - 1) * (PRE2 + 1)>(ages.sum);
+        ST2 s;
+        s.read(ring_p + tail * ST2::BYTES, lane);
+        if (!ST2::EARLY) s.multiply(acc, lane);
+        reads_done();
+        tail = tail + 1 == S2 ? 0 : tail + 1;
+        if (copies > 0) copy();
+        if (ST2::EARLY) s.multiply(acc, lane);
+        --left;
+        if (++st == C2 || left == 0) {  // the block's products, times the routing weights, to their tokens
+          const Block b = block(blk);
+          if (r < b.n) {
+            const int token = s_row[b.pos + r] >> 16;
+            const float w = s_roww[b.pos + r];
+            float* to = mine + token * R2 + 4 * q;
 #pragma unroll
-              for (int t = 0; t < ST2::RT; ++t)
-                if (R2 - 16 * t >= 16 || q < 2) {
-                  f32x4_t v = *reinterpret_cast<f32x4_t*>(to + 16 * t);
+            for (int t = 0; t < ST2::RT; ++t)
+              if (R2 - 16 * t >= 16 || q < 2) {
+                f32x4_t v = *reinterpret_cast<f32x4_t*>(to + 16 * t);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) v[i] += w * acc[t][i];
-                  *reinterpret_cast<f32x4_t*>(to + 16 * t) = v;
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < ST2::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            st = 0;
-            ++blk;
+                for (int i = 0; i < 4; ++i) v[i] += w * acc[t][i];
+                *reinterpret_cast<f32x4_t*>(to + 16 * t) = v;
+              }
           }
+#pragma unroll
+          for (int t = 0; t < ST2::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          st = 0;
+          ++blk;
         }
       }
       lds_barrier();
@@ -747,10 +745,12 @@ hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
     return wide ? run<0, MAX_T, 12, 16, 24, 1, 8, 10752>(p, grid, s) : run<0, MAX_T, 12, 16, 8, 2, 8, 10752>(p, grid, s);
   } else {
     // (twelve waves where their registers hold a stage of the smaller groups' scales too)
-    constexpr int W2 = GRP == 32 ? 8 : 12, RING2 = GRP == 32 ? 14592 : 11264;
-    if (p.T <= 2) return wide ? run<GRP, 2, 2, 16, 24, 1, W2, RING2>(p, grid, s) : run<GRP, 2, 2, 16, 8, 1, W2, RING2>(p, grid, s);
-    constexpr int W16 = GRP == 128 ? 12 : 8, RING16 = GRP == 128 ? 10752 : 16384;
-    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, W16, RING16>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, W16, RING16>(p, grid, s);
+    constexpr int W2 = GRP == 128 ? 12 : 8, RING2 = GRP == 128 ? 11264 : 16384;
+    if (p.T <= 2) return wide ? run<GRP, 2, 2, 32, 24, 1, W2, RING2>(p, grid, s) : run<GRP, 2, 2, 32, 8, 1, W2, RING2>(p, grid, s);
+    // 16 channels of f an item where that leaves four items and more to a workgroup.
+    if (p.T <= 16 && (int64_t)std::min(p.NL, p.T * p.k) * (p.f / 16) >= 4 * grid)
+      return wide ? run<GRP, 16, 4, 32, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 32, 8, 1, 8, 16384>(p, grid, s);
+    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8, 16384>(p, grid, s);
     constexpr int RB = GRP == 128 ? 4 : 3;
     return wide ? run<GRP, MAX_T, RB, 16, 24, 1, 8, 10752>(p, grid, s) : run<GRP, MAX_T, RB, 16, 8, 1, 8, 10752>(p, grid, s);
   }

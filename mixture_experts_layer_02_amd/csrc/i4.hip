@@ -224,9 +224,10 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
     wait_younger<(S - 1) * (ST::WI + ST::SI + ST::XI)>((min(i + S, mine) - i - 1) * per);
     ST st;
     st.read(ring_p + slot * ST::BYTES, lane);
-    st.multiply(acc, ring_p + slot * ST::BYTES, lane);
+    if (!ST::EARLY) st.multiply(acc, lane);
     reads_done();
     if (i + S < mine) copy(i + S, slot);
+    if (ST::EARLY) st.multiply(acc, lane);
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   // Partial sums [wave][row][channel] over the ring, once every wave is done with it.

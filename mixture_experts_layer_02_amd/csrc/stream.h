@@ -77,6 +77,9 @@ struct Stage {
   static constexpr int XROW = KS * 2, XB = RB * XROW, XI = (XB + 1023) / 1024;  // (a row's pieces lie together)
   static constexpr int BYTES = WB + SB + XB;
   static constexpr int STEPS = SUB * KC / 32;  // products of 32 k
+  // Whether a stage stays in registers while its slot is copied over, before it
+  // is multiplied; else (too many) it is multiplied first.
+  static constexpr bool EARLY = !I4 || (RT == 1 && GRP > 32);
   static_assert(!I4 || SUB == 1, "one piece of a 4-bit row per stage");
   static_assert(R % 8 == 0 && (!DUAL || R % 16 == 0), "rows");
 
@@ -102,6 +105,7 @@ struct Stage {
   // A piece of a row that lies past K, or a row past `rows`, is not read.
   template <bool EDGE>
   static __device__ __forceinline__ void copy_w_as(const Source& s, int k0, uint32_t slot, int lane) {
+    if (GRP == 32) asm volatile("" : "+v"(lane));  // (its many offsets computed here: kept over the loop they spill)
     const int r8 = lane >> 3, piece = ((lane & 7) ^ (r8 & 6)) * 16;
     const int at = I4 ? k0 / 2 : k0 * 2, left = (I4 ? (s.K / 2 + 15) & ~15 : s.K * 2) - at;  // bytes of the row from at on
     const i32x4 w[2] = {scalar(s.w[0]), DUAL ? scalar(s.w[1]) : i32x4{}};
@@ -159,9 +163,19 @@ struct Stage {
   bf16x8 b[STEPS];
   u32x4_t a[I4 ? 1 : STEPS][I4 ? 1 : RT];
   uint32_t c[I4 ? RT : 1][8];
+  f32x4_t sc[I4 && EARLY ? GPC : 1][I4 && EARLY ? RT : 1];
+  const uint8_t* from;
+
+  // The scales of group g's result rows of tile t.
+  __device__ __forceinline__ f32x4_t scale(int g, int t, int lane) const {
+    const int q = lane >> 4, part = DUAL ? q >> 1 : 0;
+    const int row = DUAL ? 8 * t + 4 * (q & 1) : 16 * t + 4 * (R - 16 * t < 16 ? q & 1 : q);
+    return *reinterpret_cast<const f32x4_t*>(from + WB + part * SIP * 256 + (g * PR + row) * 4);
+  }
 
   __device__ __forceinline__ void read(const uint8_t* slot, int lane) {
     const int r = lane & 15, q = lane >> 4, col = r % RB;
+    from = slot;
     auto xb = [&](int sub, int piece) {
       return *reinterpret_cast<const bf16x8*>(slot + WB + SB + col * XROW + sub * (KC * 2) + x_pos(piece, col) * 16);
     };
@@ -184,19 +198,24 @@ struct Stage {
       for (int t = 0; t < RT; ++t) {
         const int row = 16 * t + (R - 16 * t < 16 ? r & 7 : r);  // (half a tile: its rows twice)
         const uint8_t* w = slot + row * 128;
-        auto at = [&](int word) { return w + (((word >> 2) ^ (row & 6)) << 4) + (word & 3) * 4; };
+        // A lane's words of group g; the part of the place that is the same in every row apart (an immediate offset).
+        auto at = [&](int g) {
+          const int word = g * 4 * NJ + q * NJ, low = NJ == 1 ? g & 1 : 0;
+          return w + ((((word >> 2) - low) ^ (row & 6)) << 4) + (word & 3) * 4 + low * 16;
+        };
 #pragma unroll
         for (int g = 0; g < GPC; ++g) {
           if constexpr (NJ == 4) {
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(16 * g + 4 * q));
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(g));
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[t][4 * g + j] = v[j];
           } else if constexpr (NJ == 2) {
-            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at(8 * g + 2 * q));
+            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at(g));
             c[t][2 * g] = v[0], c[t][2 * g + 1] = v[1];
           } else {
-            c[t][g] = *reinterpret_cast<const uint32_t*>(at(4 * g + q));
+            c[t][g] = *reinterpret_cast<const uint32_t*>(at(g));
           }
+          if constexpr (EARLY) sc[g][t] = scale(g, t, lane);
         }
       }
     }
@@ -209,7 +228,7 @@ struct Stage {
     return __builtin_bit_cast(bf16x8, v);
   }
 
-  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RT], const uint8_t* slot, int lane) const {
+  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RT], int lane) const {
     if constexpr (!I4) {
 #pragma unroll
       for (int st = 0; st < STEPS; ++st)
@@ -244,13 +263,13 @@ struct Stage {
         for (int g = 0; g < GB; ++g)
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
-            const int q = lane >> 4, part = DUAL ? q >> 1 : 0;
-            const int row = DUAL ? 8 * t + 4 * (q & 1) : 16 * t + 4 * (R - 16 * t < 16 ? q & 1 : q);
-            const f32x4_t sc =
-                *reinterpret_cast<const f32x4_t*>(slot + WB + part * SIP * 256 + ((g0 + g) * PR + row) * 4);
+            f32x4_t v;
+            if constexpr (EARLY) v = sc[g0 + g][t];
+            else v = scale(g0 + g, t, lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] += sc[i] * p[g][t][i];
+            for (int i = 0; i < 4; ++i) acc[t][i] += v[i] * p[g][t][i];
           }
+        if (!EARLY) __builtin_amdgcn_sched_barrier(0);  // (else the scales of all groups are held at once, and spill)
       }
     }
   }
