@@ -219,27 +219,28 @@ __device__ __forceinline__ void route_token(const DecodeParams& p, int t, int la
 
 // GRP 0: bf16 weights.  TMAX tokens at most, RB of them in a pass over an expert's
 // rows.  R1 rows (half gate, half up) a stage in phase 1, R2 by SUB2 pieces of 128
-// bytes in phase 2; W streaming waves with RINGW bytes of ring each.
-template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int RINGW>
+// bytes in phase 2; W streaming waves.  POOL bytes of LDS hold their rings and, before
+// them, phase 1's partial sums or phase 2's sums per token.
+template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int POOL>
 __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   using namespace stream;
   using ST1 = Stage<GRP, R1, 1, true, RB>;
   using ST2 = Stage<GRP, R2, SUB2, false, RB>;
-  constexpr int S1 = RINGW / ST1::BYTES < 8 ? RINGW / ST1::BYTES : 8, S2 = RINGW / ST2::BYTES < 8 ? RINGW / ST2::BYTES : 8;
   constexpr int PRE1 = ST1::WI + ST1::SI, PRE2 = ST2::WI + ST2::SI;  // copies of a stage's weights
   constexpr int RP = R1 + 4;  // pitch of phase 1's partial sums (floats)
-  constexpr int RED = 2 * W * RB * RP * 4, YACC = W * TMAX * R2 * 4, ACC = RED > YACC ? RED : YACC;
-  constexpr int RING = W * RINGW, NT = 64 * (W + 1);
+  constexpr int RED = (2 * W * RB * RP * 4 + 1023) / 1024 * 1024, YACC = (W * TMAX * R2 * 4 + 1023) / 1024 * 1024;
+  constexpr int ACC = RED > YACC ? RED : YACC, NT = 64 * (W + 1);
+  constexpr int RINGW1 = (POOL - RED) / W / 128 * 128, RINGW2 = (POOL - ACC) / W / 128 * 128;  // of a wave
+  constexpr int S1 = RINGW1 / ST1::BYTES < 8 ? RINGW1 / ST1::BYTES : 8, S2 = RINGW2 / ST2::BYTES < 8 ? RINGW2 / ST2::BYTES : 8;
   constexpr int ROWS = TMAX * MAX_K, EXPERTS = ROWS < MAX_E ? ROWS : MAX_E;
   // (an expert of n rows has at most 1 + (n - 1) / RB blocks)
   constexpr int BLOCKS = EXPERTS + (TMAX <= RB ? 0 : (ROWS - EXPERTS) / RB);
   // Scratch of the selection, over the ring before it starts.
   constexpr int O_IDX = 0, O_W = O_IDX + ROWS * 4, O_MASK = O_W + ROWS * 4, O_BASE = O_MASK + MAX_E * 8,
                 O_KEY = O_BASE + MAX_E * 2, KEYS = MAX_E + 2 * MAX_K, SCRATCH = O_KEY + (W + 1) * KEYS * 4;
-  static_assert(SCRATCH <= RING, "scratch");
+  static_assert(SCRATCH <= POOL, "scratch");
   static_assert(S1 >= 2 && S2 >= 2, "stages");
-  __shared__ __attribute__((aligned(1024))) uint8_t ring_m[RING];
-  __shared__ __attribute__((aligned(16))) uint8_t acc_m[ACC];
+  __shared__ __attribute__((aligned(1024))) uint8_t pool[POOL];
   __shared__ Block s_blk[BLOCKS];
   __shared__ float s_roww[ROWS];
   __shared__ uint32_t s_row[ROWS];  // slots (low 16 bits) and tokens of the rows, by expert
@@ -252,10 +253,10 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   const int G = gridDim.x, slots = p.T * p.k;
 
   // ---- the selection, and the rows by expert
-  int32_t* l_idx = reinterpret_cast<int32_t*>(ring_m + O_IDX);
-  float* l_w = reinterpret_cast<float*>(ring_m + O_W);
-  unsigned long long* l_mask = reinterpret_cast<unsigned long long*>(ring_m + O_MASK);
-  uint16_t* l_base = reinterpret_cast<uint16_t*>(ring_m + O_BASE);
+  int32_t* l_idx = reinterpret_cast<int32_t*>(pool + O_IDX);
+  float* l_w = reinterpret_cast<float*>(pool + O_W);
+  unsigned long long* l_mask = reinterpret_cast<unsigned long long*>(pool + O_MASK);
+  uint16_t* l_base = reinterpret_cast<uint16_t*>(pool + O_BASE);
   int number = 0;
   if (tid == 64 * W) number = (int)__hip_atomic_fetch_add(p.sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   for (int i = tid; i < p.NL; i += NT) l_mask[i] = 0;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     // Up to a token a wave: every workgroup selects for all.  More: one workgroup
     // each, and the others wait for its flag, but not for long: if it has not
     // started, they select for themselves.
-    uint32_t* keys = reinterpret_cast<uint32_t*>(ring_m + O_KEY) + wave * KEYS;
+    uint32_t* keys = reinterpret_cast<uint32_t*>(pool + O_KEY) + wave * KEYS;
     const bool shared = p.T > W + 1;
     uint64_t todo = ~0ull >> (64 - p.T);  // tokens to select for here
     if (shared) {
@@ -388,8 +389,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     }
   };
 
-  float* red = reinterpret_cast<float*>(acc_m);
-  float* yacc = reinterpret_cast<float*>(acc_m);
+  float* red = reinterpret_cast<float*>(pool);
+  float* yacc = reinterpret_cast<float*>(pool);
   bool lost = false;  // the other workgroups' h did not come: see below
   int nmore = 0;
 
@@ -500,8 +501,11 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     asm volatile("" : "+s"(a));
     return a;
   };
-  const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)ring_m) + wave * RINGW;
-  const uint8_t* ring_p = ring_m + wave * RINGW;
+  // (Phase 2's rings may lie over other waves' of phase 1: a wave copies into its own
+  // after the last barrier of phase 1, when all have read theirs.)
+  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)pool);
+  const uint32_t ring1 = base + RED + wave * RINGW1, ring2 = base + ACC + wave * RINGW2;
+  const uint8_t *ring1_p = pool + RED + wave * RINGW1, *ring2_p = pool + ACC + wave * RINGW2;
   Ages ages;
 
   // Phase 2's share: of the item's stages (blocks by stages of a row of f) a
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
                       xr1[n] = (s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] >> 16) * (uint32_t)d * 2;
                   }
                   const int k0 = (s0 + c_at) * ST1::KS;
-                  const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST1::BYTES);
+                  const uint32_t at = __builtin_amdgcn_readfirstlane(ring1 + head * ST1::BYTES);
                   ST1::copy_w(src, k0, at, lane);
                   ages.push(PRE1 + ST1::copy_x(src, xr1, rows1, k0, at, lane));
                   head = head + 1 == S1 ? 0 : head + 1;
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         ages.pop();
         wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
         ST1 s;
-        s.read(ring_p + tail * ST1::BYTES, lane);
+        s.read(ring1_p + tail * ST1::BYTES, lane);
         if (!ST1::EARLY) s.multiply(acc, lane);
         reads_done();
         tail = tail + 1 == S1 ? 0 : tail + 1;
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 #pragma nounroll
       for (int i = 0; i < ahead; ++i) {
         if (c_new) source2(c_item, c_blk);
-        ST2::copy_w(src, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring + i * ST2::BYTES), lane);
+        ST2::copy_w(src, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring2 + i * ST2::BYTES), lane);
         next2();
       }
     }
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 #pragma nounroll
     for (; head < ahead; ++head) {  // their rows of h
       if (c_new) source2(c_item, c_blk);
-      ages.push(ST2::copy_x(src, xr2, rows2, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring + head * ST2::BYTES), lane));
+      ages.push(ST2::copy_x(src, xr2, rows2, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring2 + head * ST2::BYTES), lane));
       next2();
     }
     ahead = 0;
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     float* mine = yacc + wave * p.T * R2;
     auto copy = [&]() {
       if (c_new) source2(c_item, c_blk);
-      const uint32_t at = __builtin_amdgcn_readfirstlane(ring + head * ST2::BYTES);
+      const uint32_t at = __builtin_amdgcn_readfirstlane(ring2 + head * ST2::BYTES);
       const int k0 = c_st * ST2::KS;
       ST2::copy_w(src, k0, at, lane);
       ages.push(PRE2 + ST2::copy_x(src, xr2, rows2, k0, at, lane));
@@ -682,7 +686,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         ages.pop();
         wait_younger<(S2 - 1) * (PRE2 + 1)>(ages.sum);
         ST2 s;
-        s.read(ring_p + tail * ST2::BYTES, lane);
+        s.read(ring2_p + tail * ST2::BYTES, lane);
         if (!ST2::EARLY) s.multiply(acc, lane);
         reads_done();
         tail = tail + 1 == S2 ? 0 : tail + 1;
@@ -728,9 +732,10 @@ int64_t part_bytes(const moe_desc& d) { return align256((int64_t)router_parts(d)
 constexpr int64_t SYNC_BYTES = 4096;
 constexpr int MAX_WGS = SYNC_BYTES / 4 - SYNC_FLAGS;
 
-template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int RINGW>
+template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W>
 hipError_t run(const DecodeParams& p, int grid, hipStream_t s) {
-  decode_kernel<GRP, TMAX, RB, R1, R2, SUB2, W, RINGW><<<(unsigned)grid, 64 * (W + 1), 0, s>>>(p);
+  constexpr int POOL = TMAX > 16 ? 132 * 1024 : TMAX > 2 ? 147 * 1024 : 148 * 1024;
+  decode_kernel<GRP, TMAX, RB, R1, R2, SUB2, W, POOL><<<(unsigned)grid, 64 * (W + 1), 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -740,19 +745,19 @@ hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
   auto busiest = [&](int r2) { return ((p.d + r2 - 1) / r2 + grid - 1) / grid * r2; };
   const bool wide = busiest(24) <= busiest(8);
   if constexpr (GRP == 0) {
-    if (p.T <= 2) return wide ? run<0, 2, 2, 16, 24, 1, 8, 16384>(p, grid, s) : run<0, 2, 2, 16, 8, 3, 8, 16384>(p, grid, s);
-    if (p.T <= 16) return wide ? run<0, 16, 16, 16, 24, 1, 8, 16384>(p, grid, s) : run<0, 16, 16, 16, 8, 2, 8, 16384>(p, grid, s);
-    return wide ? run<0, MAX_T, 12, 16, 24, 1, 8, 10752>(p, grid, s) : run<0, MAX_T, 12, 16, 8, 2, 8, 10752>(p, grid, s);
+    if (p.T <= 2) return wide ? run<0, 2, 2, 16, 24, 1, 8>(p, grid, s) : run<0, 2, 2, 16, 8, 3, 8>(p, grid, s);
+    if (p.T <= 16) return wide ? run<0, 16, 16, 16, 24, 1, 8>(p, grid, s) : run<0, 16, 16, 16, 8, 2, 8>(p, grid, s);
+    return wide ? run<0, MAX_T, 12, 16, 24, 1, 8>(p, grid, s) : run<0, MAX_T, 12, 16, 8, 2, 8>(p, grid, s);
   } else {
     // (twelve waves where their registers hold a stage of the smaller groups' scales too)
-    constexpr int W2 = GRP == 128 ? 12 : 8, RING2 = GRP == 128 ? 11264 : 16384;
-    if (p.T <= 2) return wide ? run<GRP, 2, 2, 32, 24, 1, W2, RING2>(p, grid, s) : run<GRP, 2, 2, 32, 8, 1, W2, RING2>(p, grid, s);
+    constexpr int W2 = GRP == 128 ? 12 : 8;
+    if (p.T <= 2) return wide ? run<GRP, 2, 2, 32, 24, 1, W2>(p, grid, s) : run<GRP, 2, 2, 32, 8, 1, W2>(p, grid, s);
     // 16 channels of f an item where that leaves four items and more to a workgroup.
     if (p.T <= 16 && (int64_t)std::min(p.NL, p.T * p.k) * (p.f / 16) >= 4 * grid)
-      return wide ? run<GRP, 16, 4, 32, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 32, 8, 1, 8, 16384>(p, grid, s);
-    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8, 16384>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8, 16384>(p, grid, s);
+      return wide ? run<GRP, 16, 4, 32, 24, 1, 8>(p, grid, s) : run<GRP, 16, 4, 32, 8, 1, 8>(p, grid, s);
+    if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8>(p, grid, s);
     constexpr int RB = GRP == 128 ? 4 : 3;
-    return wide ? run<GRP, MAX_T, RB, 16, 24, 1, 8, 10752>(p, grid, s) : run<GRP, MAX_T, RB, 16, 8, 1, 8, 10752>(p, grid, s);
+    return wide ? run<GRP, MAX_T, RB, 32, 24, 1, 8>(p, grid, s) : run<GRP, MAX_T, RB, 32, 8, 1, 8>(p, grid, s);
   }
 }
 
