@@ -17,16 +17,26 @@ namespace {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Position of a row's word: thread i of the grid has word i % wpr of row i / wpr,
-// where wpr counts whole groups (a group's lanes lie together).  The row of the
-// workgroup's first thread in 64 bits once, then 32.
-__device__ __forceinline__ void word_of(int64_t tile, uint32_t wpr, int64_t& row, uint32_t& word) {
-  const uint64_t first = (uint64_t)tile * 256;
-  const uint64_t r0 = first / wpr;
-  const uint32_t w = (uint32_t)(first - r0 * wpr) + threadIdx.x;
-  row = (int64_t)r0 + w / wpr;
-  word = w % wpr;
-}
+// A thread's place among the pieces of all rows: piece i of the grid's threads is
+// piece i % per of row i / per; the next one lies `step` threads on, reached with
+// adds (a division each time cost as much as the rest).
+struct Place {
+  int64_t row, rows;
+  uint32_t at, per, d_at;
+  int64_t d_row;
+  __device__ __forceinline__ Place(int64_t rows_, uint32_t per_) : rows(rows_), per(per_) {
+    const uint64_t first = (uint64_t)blockIdx.x * 256, r0 = first / per, step = (uint64_t)gridDim.x * 256;
+    const uint32_t w = (uint32_t)(first - r0 * per) + threadIdx.x;
+    row = (int64_t)r0 + w / per;
+    at = w % per;
+    d_row = (int64_t)(step / per);
+    d_at = (uint32_t)(step - (uint64_t)d_row * per);
+  }
+  __device__ __forceinline__ void next() {
+    row += d_row, at += d_at;
+    if (at >= per) at -= per, ++row;
+  }
+};
 
 // A group's codes from its largest |value| m: r = v (7 / m) is off by less than
 // 2 10^-6, so the integer nearest to r is right unless r lies within 10^-5 of a
@@ -34,132 +44,182 @@ __device__ __forceinline__ void word_of(int64_t tile, uint32_t wpr, int64_t& row
 // is nearer than 2^-29 of itself to a tie without being one.  For bf16 values,
 // of 8 bits each, 14 v = (2n + 1) m is an equation of whole numbers up to 7140
 // and a power of two, so no quotient lies within 6 10^-5 of a tie without being
-// one, and the even neighbour is 2 rint(r / 2).
+// one, and the even neighbour is 2 rint(r / 2).  r + 1.5 2^23 + 8 rounds r to
+// the nearest integer, ties to even, in the low bits of its own bit pattern.
 template <bool EXACT>
 __device__ __forceinline__ uint32_t i4_codes(const float (&v)[8], uint32_t bits) {
+  constexpr float MAGIC = 12582912.0f + 8.0f;
   const float top = __uint_as_float(bits);
-  if (bits == 0 || bits >= 0x7f800000u) return 0x88888888u;
+  const bool none = bits == 0 || bits >= 0x7f800000u;
   const bool small = top < 0x1p-100f;  // (7 / m may overflow: every quotient in 64 bits)
-  const float inv = small ? 0.f : 7.0f / top;
-  uint32_t word = 0;
+  const float inv = none || small ? 0.f : 7.0f / top;
+  uint32_t b[8];
+  float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float r = v[i] * inv;
-    float q = rintf(r);
-    if (small) {
-      q = (float)rint((double)v[i] * 7.0 / (double)top);
-    } else if (fabsf(r - q) > 0.49999f) {
-      if (EXACT) q = (float)rint((double)v[i] * 7.0 / (double)top);
-      else q = 2.f * rintf(0.5f * r);
-    }
-    word |= (uint32_t)((int)q + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
+    const float r = none ? 0.f : v[i] * inv, m = r + MAGIC;
+    b[i] = __float_as_uint(m);
+    off = fmaxf(off, fabsf(r - (m - MAGIC)));
   }
+  if (!none && (off > 0.49999f || small)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = v[i] * inv;
+      float q = rintf(r);
+      if (small) q = (float)rint((double)v[i] * 7.0 / (double)top);
+      else if (fabsf(r - q) > 0.49999f) q = EXACT ? (float)rint((double)v[i] * 7.0 / (double)top) : 2.f * rintf(0.5f * r);
+      b[i] = (uint32_t)((int)q + 8);
+    }
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) word |= (b[i] & 15u) << (4 * ((i >> 1) + 4 * (i & 1)));
   return word;
 }
 
+constexpr int UNROLL = 2;  // words of a thread that are read before the first is used
+
 // One word of codes per thread, a group's words on neighbouring lanes.  Bound
-// by HBM: b + 1/2 + 4/g bytes a value.  VEC: rows start at multiples of 16
+// by HBM, b + 1/2 + 4/g bytes a value (196608 x 1792 bf16: 222 us, 4.1 TB/s, where a
+// copy runs at 5.1; a workgroup for every 512 words, none twice: 242 us).  VEC: rows start at multiples of 16
 // bytes.
 template <typename T, int GRP, bool VEC>
 __global__ void __launch_bounds__(256) i4_quantize_kernel(const T* __restrict__ w, int64_t rows, uint32_t words,
                                                           uint32_t wpr, int64_t ldw, uint8_t* __restrict__ q,
                                                           int64_t ldq, float* __restrict__ scale, int64_t lds,
-                                                          int64_t tiles) {
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    int64_t row;
-    uint32_t word;
-    word_of(tile, wpr, row, word);
-    const bool in = row < rows && word < words;
-    float v[8];
+                                                          int64_t turns) {
+  Place at(rows, wpr);  // (wpr counts whole groups: a group's lanes lie together)
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    float v[UNROLL][8];
+    int64_t row[UNROLL];
+    uint32_t word[UNROLL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (in) {
-      const T* src = w + row * ldw + (int64_t)word * 8;
-      if constexpr (VEC && sizeof(T) == 2) {
-        Vec16<uint16_t>::load(src, v);
-      } else if constexpr (VEC) {
-        float a[4], b[4];
-        Vec16<float>::load(src, a);
-        Vec16<float>::load(src + 4, b);
+    for (int u = 0; u < UNROLL; ++u) {
+      row[u] = at.row, word[u] = at.at;
+      at.next();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-      } else {
+      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+      if (row[u] < rows && word[u] < words) {
+        const T* src = w + row[u] * ldw + (int64_t)word[u] * 8;
+        if constexpr (VEC && sizeof(T) == 2) {
+          const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = Elem<T>::ld(src, i);
+          for (int i = 0; i < 4; ++i) v[u][2 * i] = __uint_as_float(a[i] << 16), v[u][2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+        } else if constexpr (VEC) {
+          const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(src));
+          const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(src + 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = a[i], v[u][4 + i] = b[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] = Elem<T>::ld(src, i);
+        }
       }
     }
-    uint32_t top = 0;  // as bits, so that NaN > infinity > every number
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int u = 0; u < UNROLL; ++u) {
+      uint32_t top = 0;  // as bits, so that NaN > infinity > every number
 #pragma unroll
-    for (int o = GRP / 16; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, WAVE));
-    if (in) {
-      *reinterpret_cast<uint32_t*>(q + row * ldq + (int64_t)word * 4) = i4_codes<sizeof(T) == 4>(v, top);
-      if (word % (GRP / 8) == 0)
-        scale[row * lds + word / (GRP / 8)] = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                                 : __uint_as_float(top) / 7.0f;
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[u][i]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = GRP / 16; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, WAVE));
+      const uint32_t code = i4_codes<sizeof(T) == 4>(v[u], top);
+      if (row[u] < rows && word[u] < words) {
+        *reinterpret_cast<uint32_t*>(q + row[u] * ldq + (int64_t)word[u] * 4) = code;
+        if (word[u] % (GRP / 8) == 0)
+          scale[row[u] * lds + word[u] / (GRP / 8)] = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                                         : __uint_as_float(top) / 7.0f;
+      }
     }
   }
 }
 
-// One word of codes per thread -> eight values.  Bound by HBM.
+// 16 bytes of values per thread: a word's eight in bf16, half a word's four in
+// float32.  Bound by HBM (196608 x 1792 to float32: 357 us, 4.5 TB/s, to bf16 194;
+// with stores that stay in the L2 382 and 198, 1792 x 6144 to float32 15.4 in place of
+// 9.4; with as few workgroups as the quantiser 418 and 221).
 template <typename T, int GRP, bool VEC>
 __global__ void __launch_bounds__(256) i4_dequantize_kernel(const uint8_t* __restrict__ q, int64_t ldq,
                                                             const float* __restrict__ scale, int64_t lds, int64_t rows,
-                                                            uint32_t words, T* __restrict__ w, int64_t ldw,
-                                                            int64_t tiles) {
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    int64_t row;
-    uint32_t word;
-    word_of(tile, words, row, word);
-    if (row >= rows) continue;
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(q + row * ldq + (int64_t)word * 4);
-    const float s = scale[row * lds + word / (GRP / 8)];
-    float v[8];
+                                                            uint32_t pieces, T* __restrict__ w, int64_t ldw,
+                                                            int64_t turns) {
+  constexpr int N = 16 / sizeof(T), H = 8 / N;
+  Place at(rows, pieces);
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    int64_t row[UNROLL];
+    uint32_t piece[UNROLL], c[UNROLL];
+    float s[UNROLL];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = s * (float)((int)((c >> (4 * ((i >> 1) + 4 * (i & 1)))) & 15u) - 8);
-    T* dst = w + row * ldw + (int64_t)word * 8;
-    if constexpr (VEC && sizeof(T) == 2) {
-      Vec16<uint16_t>::store(dst, v);
-    } else if constexpr (VEC) {
-      *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
+    for (int u = 0; u < UNROLL; ++u) {
+      row[u] = at.row, piece[u] = at.at;
+      at.next();
+      if (row[u] >= rows) continue;
+      const uint32_t word = piece[u] / H;
+      c[u] = *reinterpret_cast<const uint32_t*>(q + row[u] * ldq + (int64_t)word * 4);
+      s[u] = scale[row[u] * lds + word / (GRP / 8)];
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) Elem<T>::st(dst, i, v[i]);
+    for (int u = 0; u < UNROLL; ++u) {
+      if (row[u] >= rows) continue;
+      const uint32_t code = c[u] >> (8 * (piece[u] % H));  // (codes 4 to 7 lie 8 bits above codes 0 to 3)
+      float v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = s[u] * (float)((int)((code >> (4 * ((i >> 1) + 4 * (i & 1)))) & 15u) - 8);
+      T* dst = w + row[u] * ldw + (int64_t)piece[u] * N;
+      if constexpr (VEC && sizeof(T) == 4) {
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(dst));
+      } else if constexpr (VEC) {
+        __builtin_nontemporal_store(u32x4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])},
+                                    reinterpret_cast<u32x4*>(dst));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) Elem<T>::st(dst, i, v[i]);
+      }
     }
   }
 }
 
-unsigned grid_of(int64_t tiles) { return (unsigned)std::min<int64_t>(tiles, (int64_t)num_cus() * 64); }
+// Workgroups for so many pieces (at most `cap`), and how often each takes UNROLL
+// of them a thread.
+void launch_size(int64_t pieces, int64_t cap, unsigned& grid, int64_t& turns) {
+  grid = (unsigned)std::min<int64_t>(cdiv(pieces, 256 * UNROLL), cap);
+  turns = cdiv(pieces, (int64_t)grid * 256 * UNROLL);
+}
 
 template <typename T, int GRP>
 hipError_t quantize(const T* w, int64_t rows, int64_t cols, int64_t ldw, uint8_t* q, int64_t ldq, float* scale,
                     int64_t lds, hipStream_t s) {
   const uint32_t words = (uint32_t)(cols / 8), wpr = (uint32_t)(cdiv(cols, GRP) * (GRP / 8));
-  const int64_t tiles = cdiv(rows * wpr, 256);
+  unsigned grid;
+  int64_t turns;
+  launch_size(rows * wpr, (int64_t)num_cus() * 32, grid, turns);
   if (ldw % (int64_t)(16 / sizeof(T)) == 0)
-    i4_quantize_kernel<T, GRP, true><<<grid_of(tiles), 256, 0, s>>>(w, rows, words, wpr, ldw, q, ldq, scale, lds, tiles);
+    i4_quantize_kernel<T, GRP, true><<<grid, 256, 0, s>>>(w, rows, words, wpr, ldw, q, ldq, scale, lds, turns);
   else
-    i4_quantize_kernel<T, GRP, false><<<grid_of(tiles), 256, 0, s>>>(w, rows, words, wpr, ldw, q, ldq, scale, lds, tiles);
+    i4_quantize_kernel<T, GRP, false><<<grid, 256, 0, s>>>(w, rows, words, wpr, ldw, q, ldq, scale, lds, turns);
   return hipGetLastError();
 }
 
 template <typename T, int GRP>
 hipError_t dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t lds, int64_t rows, int64_t cols, T* w,
                       int64_t ldw, hipStream_t s) {
-  const uint32_t words = (uint32_t)(cols / 8);
-  const int64_t tiles = cdiv(rows * words, 256);
+  const uint32_t pieces = (uint32_t)(cols / (16 / sizeof(T)));
+  unsigned grid;
+  int64_t turns;
+  launch_size(rows * pieces, 1 << 30, grid, turns);
   if (ldw % (int64_t)(16 / sizeof(T)) == 0)
-    i4_dequantize_kernel<T, GRP, true><<<grid_of(tiles), 256, 0, s>>>(q, ldq, scale, lds, rows, words, w, ldw, tiles);
+    i4_dequantize_kernel<T, GRP, true><<<grid, 256, 0, s>>>(q, ldq, scale, lds, rows, pieces, w, ldw, turns);
   else
-    i4_dequantize_kernel<T, GRP, false><<<grid_of(tiles), 256, 0, s>>>(q, ldq, scale, lds, rows, words, w, ldw, tiles);
+    i4_dequantize_kernel<T, GRP, false><<<grid, 256, 0, s>>>(q, ldq, scale, lds, rows, pieces, w, ldw, turns);
   return hipGetLastError();
 }
 
 // The linear layer: a workgroup computes RB rows x R channels over all of K, whose
-// stretches of 256 its W waves take in turn, each through a ring of S stages
-// (stream.h).
+// stretches of 256 its W waves take in turn (stream.h), each with one stage of
+// LDS: the next stretch is copied while this one is multiplied.  More stages a
+// wave cost workgroups of a CU, and were slower (one row, 6144 x 6144: 7.3 us
+// with one stage, 8.0 with two; 64 rows, 3584 x 6144: 13.1 against 15.9 with four
+// waves of two).
 struct LinearParams {
   const uint16_t* x;
   const uint8_t* w;
@@ -172,12 +232,12 @@ struct LinearParams {
   int64_t items;
 };
 
-template <int GRP, int RB, int R, int W, int S, typename OUT>
+template <int GRP, int RB, int R, int W, typename OUT>
 __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
   using namespace stream;
   using ST = Stage<GRP, R, 1, false, RB>;
   constexpr int RED = W * RB * (R + 4) * 4;
-  constexpr int RING = W * S * ST::BYTES;
+  constexpr int RING = W * ST::BYTES;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > RED ? RING : RED];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -202,33 +262,25 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
   for (int n = 0; n < ST::XI; ++n) {
     xr[n] = (uint32_t)(ST::x_row(n, lane) * p.ldx * 2);
   }
-  const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * S * ST::BYTES;
-  const uint8_t* ring_p = smem + wave * S * ST::BYTES;
-  const int chunks = (p.K + 255) / 256;
-  const int mine = (chunks - wave + W - 1) / W;  // stretches wave, wave + W, ...
-  auto copy = [&](int i, int slot) {
-    const int k0 = __builtin_amdgcn_readfirstlane((wave + W * i) * 256);
-    const uint32_t at = __builtin_amdgcn_readfirstlane(ring + slot * ST::BYTES);
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem) + wave * ST::BYTES;
+  const uint8_t* stage = smem + wave * ST::BYTES;
+  auto copy = [&](int k0) {
     ST::copy_w(src, k0, at, lane);
     ST::copy_x(src, xr, rows, k0, at, lane);
   };
-  const int per = ST::WI + ST::SI + (rows * ST::XROW + 1023) / 1024;  // copies of a stage
   f32x4_t acc[ST::RT];
 #pragma unroll
   for (int t = 0; t < ST::RT; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < S; ++i)
-    if (i < mine) copy(i, i);
-  int slot = 0;
-  for (int i = 0; i < mine; ++i) {
-    wait_younger<(S - 1) * (ST::WI + ST::SI + ST::XI)>((min(i + S, mine) - i - 1) * per);
+  if (wave * 256 < p.K) copy(wave * 256);
+  for (int k0 = wave * 256; k0 < p.K; k0 += W * 256) {
+    wait_vm<0>();
+    asm volatile("" ::: "memory");
     ST st;
-    st.read(ring_p + slot * ST::BYTES, lane);
+    st.read(stage, lane);
     if (!ST::EARLY) st.multiply(acc, lane);
     reads_done();
-    if (i + S < mine) copy(i + S, slot);
+    if (k0 + W * 256 < p.K) copy(k0 + W * 256);
     if (ST::EARLY) st.multiply(acc, lane);
-    slot = slot + 1 == S ? 0 : slot + 1;
   }
   // Partial sums [wave][row][channel] over the ring, once every wave is done with it.
   __syncthreads();
@@ -251,22 +303,30 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
   }
 }
 
-template <int GRP, int RB, int R, int W, int S, typename OUT>
+template <int GRP, int RB, int R, typename OUT>
 hipError_t run_linear(LinearParams p, hipStream_t s) {
+  constexpr int W = 8;
   p.mblocks = (int)cdiv(p.M, RB);
   p.ntiles = (int)cdiv(p.N, R);
   p.items = cdiv(p.ntiles, 8) * 8 * p.mblocks;
   const unsigned grid = (unsigned)std::min<int64_t>(p.items, 1 << 22);
-  i4_linear_kernel<GRP, RB, R, W, S, OUT><<<grid, 64 * W, 0, s>>>(p);
+  i4_linear_kernel<GRP, RB, R, W, OUT><<<grid, 64 * W, 0, s>>>(p);
   return hipGetLastError();
 }
 
+// Channels of a workgroup: 16 for up to four rows (one row, 6144 x 6144: 7.3 us, with
+// 32 channels 7.9).  For more rows the fewest of 16, 32 and 64 that need no more
+// workgroups than there are CUs, for each reads all of x: 16 rows, 6144 x 1792 5.4
+// us with 32 channels (16: 7.8, 64: 6.6), 1024 x 2048 4.5 with 16 (32: 5.0); 64 rows,
+// 3584 x 6144 13.1 with 64 (32: 16.4).
 template <int GRP, typename OUT>
 hipError_t linear(const LinearParams& p, hipStream_t s) {
-  if (p.M == 1) return run_linear<GRP, 1, 16, 8, 2, OUT>(p, s);
-  if (p.M <= 4) return run_linear<GRP, 4, 16, 8, 2, OUT>(p, s);
-  if (p.M <= 16) return run_linear<GRP, 16, 32, 4, 2, OUT>(p, s);
-  return run_linear<GRP, 16, 64, 4, 2, OUT>(p, s);
+  if (p.M == 1) return run_linear<GRP, 1, 16, OUT>(p, s);
+  if (p.M <= 4) return run_linear<GRP, 4, 16, OUT>(p, s);
+  const int64_t mblocks = cdiv(p.M, 16), cus = num_cus();
+  if (cdiv(p.N, 16) * mblocks <= cus) return run_linear<GRP, 16, 16, OUT>(p, s);
+  if (cdiv(p.N, 32) * mblocks <= cus) return run_linear<GRP, 16, 32, OUT>(p, s);
+  return run_linear<GRP, 16, 64, OUT>(p, s);
 }
 
 }  // namespace
