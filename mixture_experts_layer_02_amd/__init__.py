@@ -315,7 +315,7 @@ def _rows(t, name, dtype, dev):
 def _device(t, name):
     """The current device, which has to be t's."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():  # (torch.cuda.current_device() without its wrapper)
         raise ValueError(f"{name}: a tensor of the current device is needed, not of {t.device}")
     return dev
 

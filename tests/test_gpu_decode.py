@@ -224,13 +224,18 @@ def test_linear_past_32_bit_offsets(gpu):
 class Case:
     """A layer's inputs on the GPU and their float64 reference with its bounds."""
 
-    def __init__(self, T, d, f, E, k, e0=0, NL=None, n_groups=1, renorm=1, group=0, seed=0, bias=True, routing=None, skew=0.0):
+    def __init__(self, T, d, f, E, k, e0=0, NL=None, n_groups=1, renorm=1, group=0, seed=0, bias=True, routing=None, skew=0.0,
+                 apart=False):
         rng = np.random.default_rng(seed + 1000 * T + d)
         NL = E if NL is None else NL
         self.D = moe.make_desc(T, d, f, E, k, e0, NL, "bf16", renormalize=renorm)
         self.group, self.n_groups, self.e0, self.NL = group, n_groups, e0, NL
         self.x = _bf(rng.normal(0, 1, (T, d)) * np.exp(0.3 * rng.normal(0, 1, (T, 1))))
         self.wr = _bf(rng.normal(0, d ** -0.5, (E, d)))
+        if apart:  # (token t's logits are Wr's column t: a permutation of 0 .. E - 1, in 32nds)
+            self.x = np.eye(T, d, dtype=np.float32)
+            self.wr = np.zeros((E, d), np.float32)
+            self.wr[:, :T] = np.stack([rng.permutation(E) / 32.0 for _ in range(T)], axis=1)
         self.bias = (0.3 * rng.normal(0, 1, E) - skew * np.log(1 + np.arange(E))).astype(np.float32) if bias else None
         self.routing = routing
         self.dev = dict(x=_dev(self.x, torch.bfloat16), wr=_dev(self.wr, torch.bfloat16),
@@ -343,6 +348,23 @@ def test_decode_at_the_1t_widths(gpu, group):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("T", [1, 2, 9, 30])
+def test_decode_with_a_short_last_item(gpu, T, group):
+    """d of 24 channels an item and 8 in the last; f of less than a stage and of odd stages; one token per wave and more."""
+    c = Case(T, 6080, 64 if T < 9 else 192, 8, 2, 0, 8, 1, 1, group, seed=6)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("n_groups", [2, 3, 6, 8, 16, 32])
+def test_decode_with_any_number_of_router_groups(gpu, n_groups):
+    E, k = (192, 12) if n_groups in (3, 6) else (256, 32)
+    for T, renorm in ((1, 1), (9, 0), (20, 1)):
+        c = Case(T, 128, 64, E, k, 0, 16, n_groups, renorm, 0, seed=n_groups, bias=False, apart=True)
+        assert c.sure.all()
+        c.check(c.run())
+
+
 @pytest.mark.parametrize("group", [0, 64])
 def test_decode_with_busy_experts(gpu, group):
     """Nearly all of 60 tokens at the same experts: more rows than one tile of them holds."""
@@ -451,9 +473,9 @@ def test_decode_captured_shared_and_on_two_streams(gpu, group):
         assert torch.equal(sets[j].y, want[j])
 
 
-@pytest.mark.parametrize("group", [0, 128])
-def test_decode_beside_a_kernel_that_holds_compute_units(gpu, group):
-    c = Case(3, 1024, 512, 16, 4, 0, 16, 1, 1, group, seed=19)
+@pytest.mark.parametrize("T,group", [(3, 0), (3, 128), (64, 0), (64, 32)])
+def test_decode_beside_a_kernel_that_holds_compute_units(gpu, T, group):
+    c = Case(T, 1024, 512, 16, 4, 0, 16, 1, 1, group, seed=19)
     b = c.run()
     want = b.y.clone()
     side = torch.cuda.Stream()
@@ -464,6 +486,41 @@ def test_decode_beside_a_kernel_that_holds_compute_units(gpu, group):
         c.run(b)
         torch.cuda.synchronize()
         assert torch.equal(b.y, want)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_decode_past_32_bit_offsets(gpu, group):
+    """Experts of 33 M weights, 96 of them: 6.4 GB a matrix (4 bits: 1.6 GB); the first and the last one are taken."""
+    E, d, f, T = 96, 6144, 5440, 3
+    g = torch.Generator(device="cuda").manual_seed(25)
+    D = moe.make_desc(T, d, f, E, 2, 0, E, "bf16")
+    b = moe.DecodeBuffers(D)
+    x = torch.randn(T, d, generator=g, device=gpu).bfloat16()
+    idx = torch.tensor([[0, E - 1]] * T, dtype=torch.int32, device=gpu)
+    w = torch.tensor([[0.75, 0.25], [1.0, -0.5], [0.0, 1.0]], device=gpu)
+    host = {}
+    args = []
+    for name, rows, cols in (("w1", f, d), ("w3", f, d), ("w2", d, f)):
+        if group:
+            q = torch.empty(E, rows, cols // 2, dtype=torch.uint8, device=gpu).random_(0, 256, generator=g)
+            s = torch.rand(E, rows, -(-cols // group), generator=g, device=gpu) * 4e-3 + 2e-3
+            args += [q, s]
+            host[name] = [oracle.i4_dequantize(oracle.i4_unpack(q[e].cpu().numpy()), s[e].cpu().numpy(), group) for e in (0, E - 1)]
+        else:
+            v = torch.empty(E, rows, cols, dtype=torch.bfloat16, device=gpu)
+            for e in (0, E - 1):
+                v[e].normal_(0, 0.02, generator=g)
+            args.append(v)
+            host[name] = [to_host(v[e]).astype(np.float64) for e in (0, E - 1)]
+    if group:
+        moe.decode_i4(b, x, None, moe.Int4Experts.from_codes(*args, group=group), routing=(idx, w))
+    else:
+        moe.decode(b, x, None, *args, routing=(idx, w))
+    xh, want = to_host(x).astype(np.float64), np.zeros((T, d))
+    for i in range(2):
+        G, Uv = xh @ host["w1"][i].T, xh @ host["w3"][i].T
+        want += w.cpu().numpy().astype(np.float64)[:, i:i + 1] * ((G / (1 + np.exp(-G)) * Uv) @ host["w2"][i].T)
+    assert np.abs(to_host(b.y) - want).max() <= 2e-2 * np.abs(want).max()
 
 
 def test_a_decode_step_in_4_bits_from_bf16_weights(gpu):
