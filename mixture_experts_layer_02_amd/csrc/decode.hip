@@ -306,57 +306,81 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     for (int i = tid; i < slots; i += NT) l_idx[i] = p.idx[i], l_w[i] = p.w[i];
   }
   if (tid == 64 * W) s_vid = number;
+  const bool single = TMAX <= 2 && p.T == 1;
+  if (single && wave == 0) {  // one token: its local slots are the blocks, in their order
+    if (!p.part && lane < p.k) l_idx[lane] = p.idx[lane], l_w[lane] = p.w[lane];  // (not left to the other waves' copies)
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t e = lane < p.k ? (uint32_t)l_idx[lane] - (uint32_t)p.e0 : ~0u;
+    float w = lane < p.k ? l_w[lane] : 0.f;
+    bool first = e < (uint32_t)p.NL;
+    if (!p.part)  // (a second slot with the same expert adds its weight to the first)
+      for (int j = 0; j < p.k; ++j) {
+        if (j < lane && l_idx[j] == l_idx[lane]) first = false;
+        if (j > lane && lane < p.k && l_idx[j] == l_idx[lane]) w += l_w[j];
+      }
+    const uint64_t m = __ballot(first);
+    if (first) {
+      const int pos = __popcll(m & ((1ull << lane) - 1));
+      s_blk[pos] = Block{(uint16_t)e, 1, (uint16_t)pos, 0, 1};
+      s_row[pos] = (uint32_t)lane;
+      s_roww[pos] = w;
+    }
+    if (lane == 0) s_nblk = __popcll(m);
+    if (p.part && blockIdx.x == 0 && lane < p.k) p.idx[lane] = l_idx[lane], p.w[lane] = l_w[lane];
+  }
   __syncthreads();
-  if (p.part && p.T <= W + 1 && blockIdx.x == 0)
+  if (p.part && !single && p.T <= W + 1 && blockIdx.x == 0)
     for (int i = tid; i < slots; i += NT) p.idx[i] = l_idx[i], p.w[i] = l_w[i];
   const int vid = __builtin_amdgcn_readfirstlane(s_vid);
   if (vid >= G) return;  // (another workgroup has done this one's items)
-  for (int i = tid; i < slots; i += NT) {
-    const uint32_t e = (uint32_t)l_idx[i] - (uint32_t)p.e0;
-    if (e < (uint32_t)p.NL) atomicOr(&l_mask[e], 1ull << (i / p.k));
-  }
-  __syncthreads();
-  if (wave == 0) {  // exclusive sums of the experts' rows and blocks, 64 experts at a time
-    uint32_t before = 0;
-#pragma nounroll
-    for (int base = 0; base < p.NL; base += 64) {
-      const int e = base + lane;
-      const int n = e < p.NL ? __popcll(l_mask[e]) : 0, nb = (n + RB - 1) / RB;
-      const uint32_t mine = (uint32_t)n | (uint32_t)nb << 16;
-      uint32_t inc = mine;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t v = __shfl_up(inc, o, WAVE);
-        if (lane >= o) inc += v;
-      }
-      const uint32_t ex = before + inc - mine;
-      if (e < p.NL) l_base[e] = (uint16_t)ex;
-      for (int b = 0; b < nb; ++b)
-        s_blk[(ex >> 16) + b] = Block{(uint16_t)e, (uint16_t)min(RB, n - b * RB), (uint16_t)((ex & 0xffff) + b * RB),
-                                      (uint8_t)b, (uint8_t)nb};
-      before += __shfl(inc, 63, WAVE);
+  if (!single) {
+    for (int i = tid; i < slots; i += NT) {
+      const uint32_t e = (uint32_t)l_idx[i] - (uint32_t)p.e0;
+      if (e < (uint32_t)p.NL) atomicOr(&l_mask[e], 1ull << (i / p.k));
     }
-    if (lane == 0) s_nblk = (int)(before >> 16);
-  }
-  __syncthreads();
-  for (int i = tid; i < slots; i += NT) {
-    const uint32_t e = (uint32_t)l_idx[i] - (uint32_t)p.e0;
-    if (e >= (uint32_t)p.NL) continue;
-    const int t = i / p.k;
-    // a token's second slot with the same expert adds its weight to the first
-    bool first = true;
-    float w = l_w[i];
-    if (!p.part)
-      for (int j = t * p.k; j < (t + 1) * p.k; ++j) {
-        if (j < i && l_idx[j] == l_idx[i]) first = false;
-        if (j > i && l_idx[j] == l_idx[i]) w += l_w[j];
+    __syncthreads();
+    if (wave == 0) {  // exclusive sums of the experts' rows and blocks, 64 experts at a time
+      uint32_t before = 0;
+#pragma nounroll
+      for (int base = 0; base < p.NL; base += 64) {
+        const int e = base + lane;
+        const int n = e < p.NL ? __popcll(l_mask[e]) : 0, nb = (n + RB - 1) / RB;
+        const uint32_t mine = (uint32_t)n | (uint32_t)nb << 16;
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const uint32_t v = __shfl_up(inc, o, WAVE);
+          if (lane >= o) inc += v;
+        }
+        const uint32_t ex = before + inc - mine;
+        if (e < p.NL) l_base[e] = (uint16_t)ex;
+        for (int b = 0; b < nb; ++b)
+          s_blk[(ex >> 16) + b] = Block{(uint16_t)e, (uint16_t)min(RB, n - b * RB), (uint16_t)((ex & 0xffff) + b * RB),
+                                        (uint8_t)b, (uint8_t)nb};
+        before += __shfl(inc, 63, WAVE);
       }
-    if (!first) continue;
-    const int pos = l_base[e] + __popcll(l_mask[e] & ((1ull << t) - 1));
-    s_row[pos] = (uint32_t)i | (uint32_t)t << 16;
-    s_roww[pos] = w;
+      if (lane == 0) s_nblk = (int)(before >> 16);
+    }
+    __syncthreads();
+    for (int i = tid; i < slots; i += NT) {
+      const uint32_t e = (uint32_t)l_idx[i] - (uint32_t)p.e0;
+      if (e >= (uint32_t)p.NL) continue;
+      const int t = i / p.k;
+      // a token's second slot with the same expert adds its weight to the first
+      bool first = true;
+      float w = l_w[i];
+      if (!p.part)
+        for (int j = t * p.k; j < (t + 1) * p.k; ++j) {
+          if (j < i && l_idx[j] == l_idx[i]) first = false;
+          if (j > i && l_idx[j] == l_idx[i]) w += l_w[j];
+        }
+      if (!first) continue;
+      const int pos = l_base[e] + __popcll(l_mask[e] & ((1ull << t) - 1));
+      s_row[pos] = (uint32_t)i | (uint32_t)t << 16;
+      s_roww[pos] = w;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   // ---- items
   constexpr int PR1 = R1 / 2;
