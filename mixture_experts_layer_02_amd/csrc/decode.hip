@@ -4,11 +4,12 @@
 // At these sizes the layer streams the weights of the experts that the tokens
 // take, each byte once, and is bound by HBM; the rest is latency.  The second
 // kernel therefore has one workgroup per CU, whose waves copy weights from
-// start to end (stream.h): every workgroup selects for all tokens by itself
-// (a few hundred logits each, cheaper than a kernel or a hand-over), then
+// start to end (stream.h): every workgroup selects for all tokens by itself (a
+// few hundred logits each, cheaper than a kernel or a hand-over; of more tokens
+// than it has waves, a workgroup selects for one and flags it), then
 //   phase 1: (expert, 8 channels of f or more) items: gate and up rows over all
 //            of d, h = silu(G) U to memory as bf16,
-//   phase 2: (8 or 16 channels of d) items: for every expert hit, its W2 rows
+//   phase 2: (8 or 24 channels of d) items: for every expert hit, its W2 rows
 //            over all of f, times the routing weights, summed over the experts
 //            in LDS, so that y is written once and no atomics change its order.
 // Between the phases all of h has to be there.  Each workgroup raises a flag
@@ -231,7 +232,9 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   constexpr int RED = (2 * W * RB * RP * 4 + 1023) / 1024 * 1024, YACC = (W * TMAX * R2 * 4 + 1023) / 1024 * 1024;
   constexpr int ACC = RED > YACC ? RED : YACC, NT = 64 * (W + 1);
   constexpr int RINGW1 = (POOL - RED) / W / 128 * 128, RINGW2 = (POOL - ACC) / W / 128 * 128;  // of a wave
-  constexpr int S1 = RINGW1 / ST1::BYTES < 8 ? RINGW1 / ST1::BYTES : 8, S2 = RINGW2 / ST2::BYTES < 8 ? RINGW2 / ST2::BYTES : 8;
+  // (stages at most; as many as there is room for with the rows that they have)
+  constexpr int MOST1 = RINGW1 / ST1::bytes(1) < 8 ? RINGW1 / ST1::bytes(1) : 8;
+  constexpr int MOST2 = RINGW2 / ST2::bytes(1) < 8 ? RINGW2 / ST2::bytes(1) : 8;
   constexpr int ROWS = TMAX * MAX_K, EXPERTS = ROWS < MAX_E ? ROWS : MAX_E;
   // (an expert of n rows has at most 1 + (n - 1) / RB blocks)
   constexpr int BLOCKS = EXPERTS + (TMAX <= RB ? 0 : (ROWS - EXPERTS) / RB);
@@ -239,13 +242,13 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   constexpr int O_IDX = 0, O_W = O_IDX + ROWS * 4, O_MASK = O_W + ROWS * 4, O_BASE = O_MASK + MAX_E * 8,
                 O_KEY = O_BASE + MAX_E * 2, KEYS = MAX_E + 2 * MAX_K, SCRATCH = O_KEY + (W + 1) * KEYS * 4;
   static_assert(SCRATCH <= POOL, "scratch");
-  static_assert(S1 >= 2 && S2 >= 2, "stages");
+  static_assert(RINGW1 >= ST1::BYTES && RINGW2 >= ST2::BYTES, "a stage");
   __shared__ __attribute__((aligned(1024))) uint8_t pool[POOL];
   __shared__ Block s_blk[BLOCKS];
   __shared__ float s_roww[ROWS];
   __shared__ uint32_t s_row[ROWS];  // slots (low 16 bits) and tokens of the rows, by expert
   __shared__ uint16_t s_more[256];  // numbers taken over
-  __shared__ int s_vid, s_nblk, s_cmd;
+  __shared__ int s_vid, s_nblk, s_rows, s_cmd;
   __shared__ uint64_t s_todo;
 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       s_row[pos] = (uint32_t)lane;
       s_roww[pos] = w;
     }
-    if (lane == 0) s_nblk = __popcll(m);
+    if (lane == 0) s_nblk = __popcll(m), s_rows = 1;
     if (p.part && blockIdx.x == 0 && lane < p.k) p.idx[lane] = l_idx[lane], p.w[lane] = l_w[lane];
   }
   __syncthreads();
@@ -341,6 +344,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     __syncthreads();
     if (wave == 0) {  // exclusive sums of the experts' rows and blocks, 64 experts at a time
       uint32_t before = 0;
+      int rows = 1;
 #pragma nounroll
       for (int base = 0; base < p.NL; base += 64) {
         const int e = base + lane;
@@ -354,12 +358,15 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         }
         const uint32_t ex = before + inc - mine;
         if (e < p.NL) l_base[e] = (uint16_t)ex;
+        rows = max(rows, min(RB, n));
         for (int b = 0; b < nb; ++b)
           s_blk[(ex >> 16) + b] = Block{(uint16_t)e, (uint16_t)min(RB, n - b * RB), (uint16_t)((ex & 0xffff) + b * RB),
                                         (uint8_t)b, (uint8_t)nb};
         before += __shfl(inc, 63, WAVE);
       }
-      if (lane == 0) s_nblk = (int)(before >> 16);
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) rows = max(rows, __shfl_xor(rows, o, WAVE));
+      if (lane == 0) s_nblk = (int)(before >> 16), s_rows = rows;
     }
     __syncthreads();
     for (int i = tid; i < slots; i += NT) {
@@ -385,6 +392,11 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   // ---- items
   constexpr int PR1 = R1 / 2;
   const int nblk = __builtin_amdgcn_readfirstlane(s_nblk);
+  // The rings' stages have room for the rows of the largest block: of a few rows
+  // more of them fit.
+  const int rows = __builtin_amdgcn_readfirstlane(s_rows);
+  const int bytes1 = ST1::bytes(rows), bytes2 = ST2::bytes(rows);
+  const int S1 = min(MOST1, RINGW1 / bytes1), S2 = min(MOST2, RINGW2 / bytes2);
   const int tiles1 = p.f / PR1, n1 = nblk * tiles1, n2 = (p.d + R2 - 1) / R2;
   auto count = [&](int first, int n) { return first < n ? (n - 1 - first) / G + 1 : 0; };  // items first, first + G, ..
   auto block = [&](int b) {  // (uniform)
@@ -614,7 +626,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
                       xr1[n] = (s_row[b.pos + min(ST1::x_row(n, lane), b.n - 1)] >> 16) * (uint32_t)d * 2;
                   }
                   const int k0 = (s0 + c_at) * ST1::KS;
-                  const uint32_t at = __builtin_amdgcn_readfirstlane(ring1 + head * ST1::BYTES);
+                  const uint32_t at = __builtin_amdgcn_readfirstlane(ring1 + head * bytes1);
                   ST1::copy_w(src, k0, at, lane);
                   ages.push(PRE1 + ST1::copy_x(src, xr1, rows1, k0, at, lane));
                   head = head + 1 == S1 ? 0 : head + 1;
@@ -625,9 +637,9 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 #pragma nounroll
       while (u_n < items) {
         ages.pop();
-        wait_younger<(S1 - 1) * (PRE1 + 1)>(ages.sum);
+        wait_younger<(MOST1 - 1) * (PRE1 + 1)>(ages.sum);
         ST1 s;
-        s.read(ring1_p + tail * ST1::BYTES, lane);
+        s.read(ring1_p + tail * bytes1, lane);
         if (!ST1::EARLY) s.multiply(acc, lane);
         reads_done();
         tail = tail + 1 == S1 ? 0 : tail + 1;
@@ -653,7 +665,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 #pragma nounroll
       for (int i = 0; i < ahead; ++i) {
         if (c_new) source2(c_item, c_blk);
-        ST2::copy_w(src, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring2 + i * ST2::BYTES), lane);
+        ST2::copy_w(src, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring2 + i * bytes2), lane);
         next2();
       }
     }
@@ -678,7 +690,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 #pragma nounroll
     for (; head < ahead; ++head) {  // their rows of h
       if (c_new) source2(c_item, c_blk);
-      ages.push(ST2::copy_x(src, xr2, rows2, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring2 + head * ST2::BYTES), lane));
+      ages.push(ST2::copy_x(src, xr2, rows2, c_st * ST2::KS, __builtin_amdgcn_readfirstlane(ring2 + head * bytes2), lane));
       next2();
     }
     ahead = 0;
@@ -688,7 +700,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     float* mine = yacc + wave * p.T * R2;
     auto copy = [&]() {
       if (c_new) source2(c_item, c_blk);
-      const uint32_t at = __builtin_amdgcn_readfirstlane(ring2 + head * ST2::BYTES);
+      const uint32_t at = __builtin_amdgcn_readfirstlane(ring2 + head * bytes2);
       const int k0 = c_st * ST2::KS;
       ST2::copy_w(src, k0, at, lane);
       ages.push(PRE2 + ST2::copy_x(src, xr2, rows2, k0, at, lane));
@@ -708,9 +720,9 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 #pragma nounroll
       for (int left = per2; left > 0;) {
         ages.pop();
-        wait_younger<(S2 - 1) * (PRE2 + 1)>(ages.sum);
+        wait_younger<(MOST2 - 1) * (PRE2 + 1)>(ages.sum);
         ST2 s;
-        s.read(ring2_p + tail * ST2::BYTES, lane);
+        s.read(ring2_p + tail * bytes2, lane);
         if (!ST2::EARLY) s.multiply(acc, lane);
         reads_done();
         tail = tail + 1 == S2 ? 0 : tail + 1;
@@ -780,8 +792,10 @@ hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
     if (p.T <= 16 && (int64_t)std::min(p.NL, p.T * p.k) * (p.f / 16) >= 4 * grid)
       return wide ? run<GRP, 16, 4, 32, 24, 1, 8>(p, grid, s) : run<GRP, 16, 4, 32, 8, 1, 8>(p, grid, s);
     if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8>(p, grid, s);
-    constexpr int RB = GRP == 128 ? 4 : 3;
-    return wide ? run<GRP, MAX_T, RB, 32, 24, 1, 8>(p, grid, s) : run<GRP, MAX_T, RB, 32, 8, 1, 8>(p, grid, s);
+    // Eight rows a block.  64 tokens of 64 experts (2048 x 1024), of 96 (6144 x 1792)
+    // and of 384, 96 of them here: 134, 462 and 287 us; with four rows 191, 631 and
+    // 287; with twelve, whose sums leave the rings less room, 121, 433 and 313.
+    return wide ? run<GRP, MAX_T, 8, 32, 24, 1, 8>(p, grid, s) : run<GRP, MAX_T, 8, 32, 8, 1, 8>(p, grid, s);
   }
 }
 

@@ -76,6 +76,8 @@ struct Stage {
   static constexpr int SIP = (GPC * PR + 63) / 64, SI = SIP * PARTS, SB = SI * 256;
   static constexpr int XROW = KS * 2, XB = RB * XROW, XI = (XB + 1023) / 1024;  // (a row's pieces lie together)
   static constexpr int BYTES = WB + SB + XB;
+  // (of a stage with room for that many activation rows)
+  static constexpr __host__ __device__ int bytes(int rows) { return WB + SB + rows * XROW; }
   static constexpr int STEPS = SUB * KC / 32;  // products of 32 k
   // Whether a stage stays in registers while its slot is copied over, before it
   // is multiplied; else (too many) it is multiplied first.
