@@ -675,9 +675,10 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     if (cmd < 0) break;
     ++nmore;  // a number taken over; what was copied ahead is dropped
     cur = cmd;
-    lds_barrier();  // (2)
+    // (before the barrier: it may lie over other waves' rings of phase 1)
     wait_vm<0>();
     asm volatile("" ::: "memory");
+    lds_barrier();  // (2)
     ahead = 0;
   }
 
