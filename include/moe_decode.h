@@ -53,7 +53,10 @@ int moe_i4_dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t
  *   of 16) and lds elements apart; bias [N] float32 or NULL; y [M][N] MOE_BF16
  *   or MOE_F32 as `dtype`, rows ldy >= N elements apart.  K a multiple of 8;
  *   any M >= 0 (each 16 rows read the weights anew: for hundreds of rows
- *   dequantise them and use a bf16 product).  The nibbles and scales of a
+ *   dequantise them and use a bf16 product).  The matrix cores get the codes
+ *   plus 24, and 24 times the sum of x is taken off again: the error of a
+ *   group's sum is relative to 31 sum |x|, and a row of x that holds an infinity
+ *   or NaN, or whose 31 sum |x| leaves float32, gives NaN.  The nibbles and scales of a
  *   row's last 16 bytes past K are never used.
  *   Errors: MOE_ERR_INVALID_ARG for a NULL or misaligned pointer (ws 4-byte,
  *   the others 16-byte aligned) or sizes outside these rules;
@@ -73,7 +76,7 @@ int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes);
 /* A1 to A7 for a decode step of T <= MOE_DECODE_MAX_T tokens: router logits,
  * selection (as moe_route, or moe_route_grouped with n_groups > 1), the local
  * experts' gate/up, SwiGLU and down, and the weighted sum, in two kernels.
- * Each expert's weights are read once for up to 16 of its tokens.
+ * An expert's weights are read once for 4 to 16 of its tokens (by type and T).
  *   x [T][d] bf16, Wr [E][d] bf16, bias [E] float32 or NULL; W1, W3 [NL][f][d]
  *   and W2 [NL][d][f] bf16; topk_idx [T][k] int32 and topk_w [T][k] float32,
  *   written (slots in falling order of the logits, ties to the lower expert);
@@ -101,7 +104,7 @@ int moe_decode(const moe_desc* desc, int n_groups, const void* x, const void* Wr
  * [NL][d][f/2] bytes with scales W1s, W3s [NL][f][ceil(d/group)], W2s
  * [NL][d][ceil(f/group)], as moe_i4_quantize writes them (rows without gaps).
  * The products are of bf16 activations with whole-number codes, summed in
- * float32 per group and scaled.  MOE_ERR_UNSUPPORTED also for a group other
+ * float32 per group and scaled, as in moe_i4_linear.  MOE_ERR_UNSUPPORTED also for a group other
  * than 32, 64 or 128. */
 int moe_decode_i4(const moe_desc* desc, int group, int n_groups, const void* x, const void* Wr, const float* bias,
                   const uint8_t* W1q, const float* W1s, const uint8_t* W3q, const float* W3s, const uint8_t* W2q,

@@ -206,7 +206,7 @@ hipError_t dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t
   const uint32_t pieces = (uint32_t)(cols / (16 / sizeof(T)));
   unsigned grid;
   int64_t turns;
-  launch_size(rows * pieces, 1 << 30, grid, turns);
+  launch_size(rows * pieces, 1 << 23, grid, turns);  // (a launch has fewer than 2^32 threads)
   if (ldw % (int64_t)(16 / sizeof(T)) == 0)
     i4_dequantize_kernel<T, GRP, true><<<grid, 256, 0, s>>>(q, ldq, scale, lds, rows, pieces, w, ldw, turns);
   else
