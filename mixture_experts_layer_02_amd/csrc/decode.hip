@@ -13,7 +13,9 @@
 //            over all of f, times the routing weights, summed over the experts
 //            in LDS, so that y is written once and no atomics change its order.
 // Between the phases all of h has to be there.  Each workgroup raises a flag
-// when its phase-1 items are done and waits for all flags; the W2 copies of its
+// when its phase-1 items are done and waits for all flags (they take 3 to 4 us
+// from the last one on; looked at faster, all 256 in one go or one counter in
+// their place, the looking holds up the raising: 7 and 12 us); the W2 copies of its
 // first phase-2 items are in flight meanwhile.
 //
 // The wait needs no workgroup that is not running yet: a workgroup's items
@@ -48,7 +50,7 @@ constexpr int SYNC_TOKENS = 64, SYNC_FLAGS = SYNC_TOKENS + MAX_T;
 
 // Partial sums part[ks][t][e] of x Wr^T: a workgroup has 16 experts and a
 // gridDim.y-th of d, each of its 16 waves a sixteenth of that; 16 CT tokens.  Clears the second
-// kernel's counter and flags.
+// kernel's counters and flags.
 template <int CT>
 __global__ void __launch_bounds__(1024) decode_router_kernel(const uint16_t* __restrict__ x,
                                                             const uint16_t* __restrict__ wr, int T, int d, int E,
@@ -118,6 +120,8 @@ struct DecodeParams {
   uint32_t* sync;
   int T, d, f, E, k, e0, NL, renorm, n_groups, ks;
 };
+
+constexpr __host__ __device__ int align128(int n) { return (n + 127) / 128 * 128; }
 
 // The tokens that one pass over an expert's rows serves.
 struct alignas(8) Block {
@@ -220,33 +224,32 @@ __device__ __forceinline__ void route_token(const DecodeParams& p, int t, int la
 
 // GRP 0: bf16 weights.  TMAX tokens at most, RB of them in a pass over an expert's
 // rows.  R1 rows (half gate, half up) a stage in phase 1, R2 by SUB2 pieces of 128
-// bytes in phase 2; W streaming waves.  POOL bytes of LDS hold their rings and, before
+// bytes in phase 2; W streaming waves.  LDS holds the lists, then the rings and, before
 // them, phase 1's partial sums or phase 2's sums per token.
-template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W, int POOL>
+template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W>
 __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   using namespace stream;
   using ST1 = Stage<GRP, R1, 1, true, RB>;
   using ST2 = Stage<GRP, R2, SUB2, false, RB>;
   constexpr int PRE1 = ST1::WI + ST1::SI, PRE2 = ST2::WI + ST2::SI;  // copies of a stage's weights
   constexpr int RP = R1 + 4;  // pitch of phase 1's partial sums (floats)
-  constexpr int RED = (2 * W * RB * RP * 4 + 1023) / 1024 * 1024, YACC = (W * TMAX * R2 * 4 + 1023) / 1024 * 1024;
-  constexpr int ACC = RED > YACC ? RED : YACC, NT = 64 * (W + 1);
-  constexpr int RINGW1 = (POOL - RED) / W / 128 * 128, RINGW2 = (POOL - ACC) / W / 128 * 128;  // of a wave
+  constexpr int NT = 64 * (W + 1), LDS = 159 * 1024;
   // (stages at most; as many as there is room for with the rows that they have)
-  constexpr int MOST1 = RINGW1 / ST1::bytes(1) < 8 ? RINGW1 / ST1::bytes(1) : 8;
-  constexpr int MOST2 = RINGW2 / ST2::bytes(1) < 8 ? RINGW2 / ST2::bytes(1) : 8;
+  constexpr int MOST1 = LDS / W / ST1::bytes(1) < 8 ? LDS / W / ST1::bytes(1) : 8;
+  constexpr int MOST2 = LDS / W / ST2::bytes(1) < 8 ? LDS / W / ST2::bytes(1) : 8;
   constexpr int ROWS = TMAX * MAX_K, EXPERTS = ROWS < MAX_E ? ROWS : MAX_E;
   // (an expert of n rows has at most 1 + (n - 1) / RB blocks)
   constexpr int BLOCKS = EXPERTS + (TMAX <= RB ? 0 : (ROWS - EXPERTS) / RB);
   // Scratch of the selection, over the ring before it starts.
   constexpr int O_IDX = 0, O_W = O_IDX + ROWS * 4, O_MASK = O_W + ROWS * 4, O_BASE = O_MASK + MAX_E * 8,
                 O_KEY = O_BASE + MAX_E * 2, KEYS = MAX_E + 2 * MAX_K, SCRATCH = O_KEY + (W + 1) * KEYS * 4;
-  static_assert(SCRATCH <= POOL, "scratch");
-  static_assert(RINGW1 >= ST1::BYTES && RINGW2 >= ST2::BYTES, "a stage");
-  __shared__ __attribute__((aligned(1024))) uint8_t pool[POOL];
-  __shared__ Block s_blk[BLOCKS];
-  __shared__ float s_roww[ROWS];
-  __shared__ uint32_t s_row[ROWS];  // slots (low 16 bits) and tokens of the rows, by expert
+  // With the most rows and tokens there is room for a stage of each wave.
+  constexpr int LISTS = align128(BLOCKS * 8 + ROWS * 8);
+  static_assert(LISTS + SCRATCH <= LDS, "scratch");
+  static_assert((LDS - LISTS - align128(2 * W * RB * RP * 4)) / W / 128 * 128 >= ST1::BYTES, "a stage");
+  static_assert((LDS - LISTS - align128(2 * W * RB * RP * 4)) / W / 128 * 128 >= ST2::BYTES, "a stage");
+  static_assert((LDS - LISTS - align128(W * TMAX * R2 * 4)) / W / 128 * 128 >= ST2::BYTES, "a stage");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
   __shared__ uint16_t s_more[256];  // numbers taken over
   __shared__ int s_vid, s_nblk, s_rows, s_cmd;
   __shared__ uint64_t s_todo;
@@ -254,6 +257,17 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = gridDim.x, slots = p.T * p.k;
+  // The lists come first in LDS; the rest is phase 1's sums or phase 2's, and the
+  // rings.  Above 16 tokens they are sized for this call, not for the most that there
+  // may be, which left one stage a wave in phase 2 (64 tokens of the 4-bit share: 279 ->
+  // 267 us; for fewer tokens the sizes that are known beforehand are 0.5 us better).
+  constexpr bool SIZED = TMAX > 16;
+  const int hits = min(slots, p.NL), blocks = SIZED ? hits + (slots - hits) / RB : BLOCKS, listed = SIZED ? slots : ROWS;
+  Block* s_blk = reinterpret_cast<Block*>(smem);
+  float* s_roww = reinterpret_cast<float*>(smem + blocks * 8);
+  uint32_t* s_row = reinterpret_cast<uint32_t*>(smem + blocks * 8 + listed * 4);  // slots (low 16 bits) and tokens of the rows, by expert
+  const int lists = align128(blocks * 8 + listed * 8);
+  uint8_t* pool = smem + lists;
 
   // ---- the selection, and the rows by expert
   int32_t* l_idx = reinterpret_cast<int32_t*>(pool + O_IDX);
@@ -396,7 +410,10 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   // more of them fit.
   const int rows = __builtin_amdgcn_readfirstlane(s_rows);
   const int bytes1 = ST1::bytes(rows), bytes2 = ST2::bytes(rows);
-  const int S1 = min(MOST1, RINGW1 / bytes1), S2 = min(MOST2, RINGW2 / bytes2);
+  const int red_at = (SIZED ? rows : RB) * RP, red_bytes = align128(2 * W * red_at * 4);  // a wave's partial sums of an item, all of two items
+  const int acc_bytes = max(red_bytes, align128(W * (SIZED ? p.T : TMAX) * R2 * 4));
+  const int ringw1 = (LDS - lists - red_bytes) / W / 128 * 128, ringw2 = (LDS - lists - acc_bytes) / W / 128 * 128;
+  const int S1 = min(MOST1, ringw1 / bytes1), S2 = min(MOST2, ringw2 / bytes2);
   const int tiles1 = p.f / PR1, n1 = nblk * tiles1, n2 = (p.d + R2 - 1) / R2;
   auto count = [&](int first, int n) { return first < n ? (n - 1 - first) / G + 1 : 0; };  // items first, first + G, ..
   auto block = [&](int b) {  // (uniform)
@@ -456,14 +473,14 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         int tile;
         item1(m, b, tile);
         lds_barrier();  // the item's partial sums are in red[n % 2]
-        const float* rd = red + (n & 1) * W * RB * RP;
+        const float* rd = red + (n & 1) * W * red_at;
         // Lane l: row l / 16 of four, row l % 16 (8 gate, 8 up) of a 16-row tile.
         for (int i = 0; i < b.n * (R1 / 16); i += 4) {
           const int j = i + q, row = j / (R1 / 16), t = j % (R1 / 16);
           float v = 0.f;
           if (row < b.n) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) v += rd[(w * RB + row) * RP + 16 * t + r];
+            for (int w = 0; w < W; ++w) v += rd[w * red_at + row * RP + 16 * t + r];
           }
           const float up = __shfl_xor(v, 8, WAVE), hv = v * sigmoidf_(v) * up, other = __shfl_xor(hv, 1, WAVE);
           if (row < b.n && r < 8 && r % 2 == 0)
@@ -540,8 +557,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   // (Phase 2's rings may lie over other waves' of phase 1: a wave copies into its own
   // after the last barrier of phase 1, when all have read theirs.)
   const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)pool);
-  const uint32_t ring1 = base + RED + wave * RINGW1, ring2 = base + ACC + wave * RINGW2;
-  const uint8_t *ring1_p = pool + RED + wave * RINGW1, *ring2_p = pool + ACC + wave * RINGW2;
+  const uint32_t ring1 = base + red_bytes + wave * ringw1, ring2 = base + acc_bytes + wave * ringw2;
+  const uint8_t *ring1_p = pool + red_bytes + wave * ringw1, *ring2_p = pool + acc_bytes + wave * ringw2;
   Ages ages;
 
   // Phase 2's share: of the item's stages (blocks by stages of a row of f) a
@@ -589,8 +606,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
     if (per1 == 0) {
 #pragma nounroll
       for (int n = 0; n < items; ++n) {
-        float* rd = red + ((n & 1) * W + wave) * RB * RP;
-        for (int i = lane; i < RB * RP; i += 64) rd[i] = 0.f;
+        float* rd = red + ((n & 1) * W + wave) * red_at;
+        for (int i = lane; i < red_at; i += 64) rd[i] = 0.f;
         lds_barrier();
       }
     } else {
@@ -646,8 +663,8 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         if (c_m.i < n1) copy();
         if (ST1::EARLY) s.multiply(acc, lane);
         if (++u_at == per1) {
-          float* rd = red + ((u_n & 1) * W + wave) * RB * RP;
-          if (r < RB) {
+          float* rd = red + ((u_n & 1) * W + wave) * red_at;
+          if (r < (SIZED ? rows : RB)) {
 #pragma unroll
             for (int t = 0; t < ST1::RT; ++t) *reinterpret_cast<f32x4_t*>(rd + r * RP + 16 * t + 4 * q) = acc[t];
           }
@@ -767,12 +784,11 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 int router_parts(const moe_desc& d) { return d.d >= 1024 ? 4 : 1; }
 int64_t part_bytes(const moe_desc& d) { return align256((int64_t)router_parts(d) * d.T * d.E * 4); }
 constexpr int64_t SYNC_BYTES = 4096;
-constexpr int MAX_WGS = SYNC_BYTES / 4 - SYNC_FLAGS;
+constexpr int MAX_WGS = 256;  // (a workgroup may take over all the others' numbers)
 
 template <int GRP, int TMAX, int RB, int R1, int R2, int SUB2, int W>
 hipError_t run(const DecodeParams& p, int grid, hipStream_t s) {
-  constexpr int POOL = TMAX > 16 ? 132 * 1024 : TMAX > 2 ? 147 * 1024 : 148 * 1024;
-  decode_kernel<GRP, TMAX, RB, R1, R2, SUB2, W, POOL><<<(unsigned)grid, 64 * (W + 1), 0, s>>>(p);
+  decode_kernel<GRP, TMAX, RB, R1, R2, SUB2, W><<<(unsigned)grid, 64 * (W + 1), 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -282,8 +282,13 @@ struct Stage {
 template <int COMMON>
 __device__ __forceinline__ void wait_younger(int n) {
   if (n == COMMON) wait_vm<COMMON>();
-  else if (n >= 16) n >= 32 ? wait_vm<32>() : n >= 24 ? wait_vm<24>() : n >= 20 ? wait_vm<20>() : wait_vm<16>();
-  else if (n >= 8) n >= 12 ? wait_vm<12>() : n >= 10 ? wait_vm<10>() : wait_vm<8>();
+  else if (n >= 16) {
+    if (n >= 24) n >= 32 ? wait_vm<32>() : n >= 28 ? wait_vm<28>() : wait_vm<24>();
+    else n >= 21 ? wait_vm<21>() : n >= 18 ? wait_vm<18>() : wait_vm<16>();
+  } else if (n >= 8) {
+    if (n >= 12) n >= 14 ? wait_vm<14>() : wait_vm<12>();
+    else n >= 10 ? wait_vm<10>() : wait_vm<8>();
+  }
   else if (n >= 4) n >= 6 ? wait_vm<6>() : n >= 5 ? wait_vm<5>() : wait_vm<4>();
   else n >= 3 ? wait_vm<3>() : n >= 2 ? wait_vm<2>() : n >= 1 ? wait_vm<1>() : wait_vm<0>();
   asm volatile("" ::: "memory");
