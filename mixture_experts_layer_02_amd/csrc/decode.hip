@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // Parts of d in the logits' partial sums (1 or 4, see route_token): more of them
 // spread the router's weights over more CUs (64 tokens, 384 experts of 6144: 24 us
-// with one part).
+// with one part, 9 with four).
 int router_parts(const moe_desc& d) { return d.d >= 1024 ? 4 : 1; }
 int64_t part_bytes(const moe_desc& d) { return align256((int64_t)router_parts(d) * d.T * d.E * 4); }
 constexpr int64_t SYNC_BYTES = 4096;

@@ -391,6 +391,16 @@ def test_decode_with_a_given_routing(gpu, group):
     assert (to_host(c1.run().y) == 0).all()
 
 
+@pytest.mark.parametrize("T,group", [(64, 0), (64, 32), (64, 64), (64, 128), (16, 0), (16, 128)])
+def test_decode_with_the_longest_lists(gpu, T, group):
+    """32 picks a token: half of the tokens name every expert once, the others all the same 32."""
+    E, k = 16 * T, 32
+    idx = np.concatenate([np.arange(E).reshape(T // 2, k), np.tile(np.arange(k)[::-1], (T // 2, 1))]).astype(np.int32)
+    w = _bf(np.random.default_rng(T).uniform(0.01, 0.1, (T, k)))
+    c = Case(T, 64, 128, E, k, 0, E, 1, 1, group, seed=T, routing=(idx, w))
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("n_groups", [1, 4])
 def test_decode_gives_ties_to_the_lower_expert(gpu, n_groups):
     """Logits of small whole numbers, equal by the dozen."""
