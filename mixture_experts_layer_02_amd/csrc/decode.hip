@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   // more of them fit.
   const int rows = __builtin_amdgcn_readfirstlane(s_rows);
   const int bytes1 = ST1::bytes(rows), bytes2 = ST2::bytes(rows);
+  const int col = ST1::column(lane, rows);  // (of ST2 too; RB - 1 in its place would read past the last wave's ring, and LDS)
   const int red_at = (SIZED ? rows : RB) * RP, red_bytes = align128(2 * W * red_at * 4);  // a wave's partial sums of an item, all of two items
   const int acc_bytes = max(red_bytes, align128(W * (SIZED ? p.T : TMAX) * R2 * 4));
   const int ringw1 = (LDS - lists - red_bytes) / W / 128 * 128, ringw2 = (LDS - lists - acc_bytes) / W / 128 * 128;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         ages.pop();
         wait_younger<(MOST1 - 1) * (PRE1 + 1)>(ages.sum);
         ST1 s;
-        s.read(ring1_p + tail * bytes1, lane);
+        s.read(ring1_p + tail * bytes1, lane, col);
         if (!ST1::EARLY) s.multiply(acc, lane);
         reads_done();
         tail = tail + 1 == S1 ? 0 : tail + 1;
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
         ages.pop();
         wait_younger<(MOST2 - 1) * (PRE2 + 1)>(ages.sum);
         ST2 s;
-        s.read(ring2_p + tail * bytes2, lane);
+        s.read(ring2_p + tail * bytes2, lane, col);
         if (!ST2::EARLY) s.multiply(acc, lane);
         reads_done();
         tail = tail + 1 == S2 ? 0 : tail + 1;

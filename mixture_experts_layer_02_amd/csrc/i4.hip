@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
     wait_vm<0>();
     asm volatile("" ::: "memory");
     ST st;
-    st.read(stage, lane);
+    st.read(stage, lane, ST::column(lane, RB));
     if (!ST::EARLY) st.multiply(acc, lane);
     reads_done();
     if (k0 + W * 256 < p.K) copy(k0 + W * 256);

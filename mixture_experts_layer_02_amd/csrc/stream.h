@@ -161,7 +161,7 @@ struct Stage {
   }
 
   // A stage in registers, and its products added to acc (rows 16 t + 4 (l / 16)
-  // .. + 3, column l % 16; columns without a row hold anything).
+  // .. + 3, column l % 16; columns without a row repeat others or hold anything).
   bf16x8 b[STEPS];
   u32x4_t a[I4 ? 1 : STEPS][I4 ? 1 : RT];
   uint32_t c[I4 ? RT : 1][8];
@@ -175,8 +175,16 @@ struct Stage {
     return *reinterpret_cast<const f32x4_t*>(from + WB + part * SIP * 256 + (g * PR + row) * 4);
   }
 
-  __device__ __forceinline__ void read(const uint8_t* slot, int lane) {
-    const int r = lane & 15, q = lane >> 4, col = r % RB;
+  // The activation row that a lane reads, of a stage with room for `rows` (1 .. RB):
+  // lanes past them read the last one, whose bytes the stage has.
+  static __device__ __forceinline__ int column(int lane, int rows) {
+    const int col = (lane & 15) % RB;
+    return col < rows ? col : rows - 1;
+  }
+
+  // col: column(lane, rows), kept by the caller.
+  __device__ __forceinline__ void read(const uint8_t* slot, int lane, int col) {
+    const int r = lane & 15, q = lane >> 4;
     from = slot;
     auto xb = [&](int sub, int piece) {
       return *reinterpret_cast<const bf16x8*>(slot + WB + SB + col * XROW + sub * (KC * 2) + x_pos(piece, col) * 16);
