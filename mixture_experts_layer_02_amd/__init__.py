@@ -771,6 +771,7 @@ class Int4Experts:
     from W1, W3 [NL][f][d] and W2 [NL][d][f]."""
 
     def __init__(self, w1, w3, w2, group=128):
+        _group(group)
         self.group = group
         for name, w in (("w1", w1), ("w3", w3), ("w2", w2)):
             n, rows, cols = w.shape
@@ -782,7 +783,14 @@ class Int4Experts:
 
     @classmethod
     def from_codes(cls, w1q, w1s, w3q, w3s, w2q, w2s, group=128):
-        """From codes and scales that are there already (as i4_quantize writes them)."""
+        """From codes and scales that are there already (as i4_quantize writes them): the codes
+        [NL][f][d / 2] and [NL][d][f / 2], the scales [NL][f][ceil(d / group)] and [NL][d][ceil(f / group)];
+        or tensors of other shapes with exactly as many values, which are taken to lie like these."""
+        _group(group)
+        for name, q, s in (("w1s", w1q, w1s), ("w3s", w3q, w3s), ("w2s", w2q, w2s)):
+            if q.dim() == s.dim() == 3 and s.size(2) != -(-2 * q.size(2) // group):
+                raise ValueError(f"{name}: {-(-2 * q.size(2) // group)} scales a row are needed for groups of {group} in rows of "
+                                 f"{2 * q.size(2)} codes, not {s.size(2)}")
         e = cls.__new__(cls)
         e.group, e.w1q, e.w1s, e.w3q, e.w3s, e.w2q, e.w2s = group, w1q, w1s, w3q, w3s, w2q, w2s
         return e
@@ -793,13 +801,19 @@ def decode_i4(b: DecodeBuffers, x, wr, experts: Int4Experts, bias=None, routing=
     D, g = b.desc, experts.group
     NL, d, f = D.num_local, D.d, D.f
     _group(g)
-    nd, nf = NL * f * -(-d // g), NL * d * -(-f // g)
+
+    def rows(name, n, m, dtype, dev):  # (other experts' rows, or another group's scales, would be read at the wrong places)
+        t = getattr(experts, name)
+        p = _flat(t, name, NL * n * m, dtype, dev)
+        if (t.size(1) != n or t.size(2) != m) if t.dim() == 3 else t.numel() != NL * n * m:
+            raise ValueError(f"{name}: [{NL}][{n}][{m}] values are needed, not {tuple(t.shape)}")
+        return p
 
     def weights(dev):
         out = []
-        for name, ns in (("w1", nd), ("w3", nd), ("w2", nf)):
-            out.append(_flat(getattr(experts, name + "q"), name + "q", NL * f * d // 2, torch.uint8, dev))
-            out.append(_flat(getattr(experts, name + "s"), name + "s", ns, torch.float32, dev))
+        for name, n, m in (("w1", f, d), ("w3", f, d), ("w2", d, f)):
+            out.append(rows(name + "q", n, m // 2, torch.uint8, dev))
+            out.append(rows(name + "s", n, -(-m // g), torch.float32, dev))
         return out
 
     return _decode("moe_decode_i4", b, x, wr, weights, bias, routing, n_groups, g)
