@@ -89,8 +89,9 @@ int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes);
  *   moe_grouped_ffn, y once at the end.  A token whose logits are not finite
  *   may get any selection; what does not depend on it is right.
  *   ws: moe_decode_workspace_size() bytes; calls that share one must not
- *   overlap (same stream, or ordered by events).  It needs no preparation and
- *   holds nothing from call to call.  tile_schedule and wgrad_dtype are of no
+ *   overlap (same stream, or ordered by events; where they do, y is undefined, and
+ *   NaN if a call gives up, after seconds, on flags that the other has cleared).
+ *   It needs no preparation and holds nothing from call to call.  tile_schedule and wgrad_dtype are of no
  *   consequence.
  *   Errors: MOE_ERR_INVALID_ARG for a NULL or misaligned pointer or a bad
  *   descriptor or n_groups (as moe_route_grouped); MOE_ERR_WORKSPACE for too

@@ -497,12 +497,13 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
       if (lane == 0)
         __hip_atomic_store(p.sync + SYNC_FLAGS + cur, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       // All flags up: on.  Else, after 20 us, take the number of a workgroup that
-      // has not started, if there is one.  (Ten seconds pass only where the
-      // workspace's rule is broken, and another call has cleared the flags: y is
-      // then NaN, and the kernel ends.)
+      // has not started, if there is one.  (So many looks, 1 to 2 us each, pass only
+      // where the workspace's rule is broken, and another call has cleared the flags: y
+      // is then NaN, and the kernel ends.  Looks and not time: the clock runs on while
+      // a queue is off the GPU.)
       int cmd = -1;
       const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
-      for (;;) {
+      for (int looks = 0;; ++looks) {
         bool all = true;
         for (int i = lane; i < G; i += 64)
           all &= __hip_atomic_load(p.sync + SYNC_FLAGS + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0;
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
           }
           take = false;
         }
-        if (dt > 1000000000ull) {
+        if (looks >= 1 << 23) {
           cmd = -2;
           break;
         }
