@@ -54,10 +54,11 @@ int moe_i4_dequantize(const uint8_t* q, int64_t ldq, const float* scale, int64_t
  *   or MOE_F32 as `dtype`, rows ldy >= N elements apart.  K a multiple of 8;
  *   any M >= 0 (each 16 rows read the weights anew: for hundreds of rows
  *   dequantise them and use a bf16 product).  The matrix cores get the codes
- *   plus 24, and 24 times the sum of x is taken off again: the error of a
- *   group's sum is relative to 31 sum |x|, and a row of x that holds an infinity
- *   or NaN, or whose 31 sum |x| leaves float32, gives NaN.  The nibbles and scales of a
- *   row's last 16 bytes past K are never used.
+ *   plus 24, and 24 times the sum of x is taken off again: the rounding error of
+ *   a group's sum is relative to up to (24 + 31) sum |x|.  No sum on the way is
+ *   above 31 sum |x|; a row of x for which that leaves float32 may give NaN, and
+ *   one that holds an infinity or NaN does.  The nibbles and scales of a row's
+ *   last 16 bytes past K are never used.
  *   Errors: MOE_ERR_INVALID_ARG for a NULL or misaligned pointer (ws 4-byte,
  *   the others 16-byte aligned) or sizes outside these rules;
  *   MOE_ERR_UNSUPPORTED for another dtype or group, K above 2^20, ldx, ldw or
@@ -76,7 +77,8 @@ int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes);
 /* A1 to A7 for a decode step of T <= MOE_DECODE_MAX_T tokens: router logits,
  * selection (as moe_route, or moe_route_grouped with n_groups > 1), the local
  * experts' gate/up, SwiGLU and down, and the weighted sum, in two kernels.
- * An expert's weights are read once for 4 to 16 of its tokens (by type and T).
+ * An expert's weights are read once for up to 4 to 16 of its tokens (by type and
+ * T; both tokens of two).
  *   x [T][d] bf16, Wr [E][d] bf16, bias [E] float32 or NULL; W1, W3 [NL][f][d]
  *   and W2 [NL][d][f] bf16; topk_idx [T][k] int32 and topk_w [T][k] float32,
  *   written (slots in falling order of the logits, ties to the lower expert);
@@ -91,12 +93,12 @@ int moe_decode_workspace_size(const moe_desc* desc, size_t* bytes);
  *   ws: moe_decode_workspace_size() bytes; calls that share one must not
  *   overlap (same stream, or ordered by events; where they do, y is undefined, and
  *   NaN if a call gives up, after seconds, on flags that the other has cleared).
- *   It needs no preparation and holds nothing from call to call.  tile_schedule and wgrad_dtype are of no
- *   consequence.
+ *   It needs no preparation and holds nothing from call to call.  tile_schedule
+ *   and wgrad_dtype are of no consequence.
  *   Errors: MOE_ERR_INVALID_ARG for a NULL or misaligned pointer or a bad
  *   descriptor or n_groups (as moe_route_grouped); MOE_ERR_WORKSPACE for too
- *   small a workspace; MOE_ERR_UNSUPPORTED for more tokens, another dtype than
- *   MOE_BF16, d or f above 2^20, or T k f of 2^30 or more. */
+ *   small or a misaligned workspace; MOE_ERR_UNSUPPORTED for more tokens,
+ *   another dtype than MOE_BF16, d or f above 2^20, or T k f of 2^30 or more. */
 int moe_decode(const moe_desc* desc, int n_groups, const void* x, const void* Wr, const float* bias, const void* W1,
                const void* W3, const void* W2, int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes,
                void* stream);

@@ -16,7 +16,7 @@
 // four registers by a shift and an and-or each.  The 24 times the sum of x that
 // comes with it is taken off by products with a constant -24, whose sum the
 // accumulator starts from.  All of it is exact but for the float32 sums, whose
-// terms are up to 56 |x| in place of 8 |x|: 3 bits of 24.
+// terms of an x are up to (24 + 31) |x| in place of 8 |x|: 3 bits of 24.
 #pragma once
 
 #include "gemm_dma.h"
