@@ -236,6 +236,7 @@ template <int GRP, int RB, int R, int W, typename OUT>
 __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
   using namespace stream;
   using ST = Stage<GRP, R, 1, false, RB>;
+  static_assert(R % 16 == 0, "whole tiles: half of one would store its rows twice");
   constexpr int RED = W * RB * (R + 4) * 4;
   constexpr int RING = W * ST::BYTES;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > RED ? RING : RED];
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(64 * W) i4_linear_kernel(LinearParams p) {
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);
   const int col = lane & 15;
-  if (col < RB && (R > 8 || lane < 32)) {
+  if (col < RB) {
 #pragma unroll
     for (int t = 0; t < ST::RT; ++t)
       *reinterpret_cast<f32x4_t*>(red + (wave * RB + col) * (R + 4) + 16 * t + 4 * (lane >> 4)) = acc[t];
