@@ -727,7 +727,9 @@ def decode_workspace_size(desc: MoeDesc) -> int:
 
 
 class DecodeBuffers:
-    """The tensors of decode and decode_i4: the selection, y and the workspace."""
+    """The tensors of decode and decode_i4: the selection, y and the workspace, for steps of
+    desc.T tokens, or fewer: set ``desc`` to one that differs in a smaller T alone, and a step
+    writes the first T rows of y, topk_idx and topk_w and leaves the others."""
 
     def __init__(self, desc: MoeDesc, device="cuda"):
         self.desc = desc
