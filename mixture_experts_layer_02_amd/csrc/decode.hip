@@ -8,7 +8,9 @@
 // few hundred logits each, cheaper than a kernel or a hand-over; of more tokens
 // than it has waves, a workgroup selects for one and flags it), then
 //   phase 1: (expert, 8 channels of f or more) items: gate and up rows over all
-//            of d, h = silu(G) U to memory as bf16,
+//            of d, h = silu(G) U to memory as bf16 (as in the layer's other forms,
+//            and what the matrix cores take: y is then 0.0024 of its rms from the
+//            exact sums, with its own rounding alone 0.0017),
 //   phase 2: (8 or 24 channels of d) items: for every expert hit, its W2 rows
 //            over all of f, times the routing weights, summed over the experts
 //            in LDS, so that y is written once and no atomics change its order.
@@ -259,8 +261,9 @@ __global__ void __launch_bounds__(64 * (W + 1)) decode_kernel(DecodeParams p) {
   const int G = gridDim.x, slots = p.T * p.k;
   // The lists come first in LDS; the rest is phase 1's sums or phase 2's, and the
   // rings.  Above 16 tokens they are sized for this call, not for the most that there
-  // may be, which left one stage a wave in phase 2 (64 tokens of the 4-bit share: 279 ->
-  // 267 us; for fewer tokens the sizes that are known beforehand are 0.5 us better).
+  // may be, which left one stage a wave in phase 2 (4 bits, in turn on one card: the share's
+  // 64 tokens 285 -> 280 us, 24 tokens of 96 experts 348 -> 331, 64 of them 456 -> 461;
+  // for fewer tokens the sizes that are known beforehand are 0.5 us better).
   constexpr bool SIZED = TMAX > 16;
   const int hits = min(slots, p.NL), blocks = SIZED ? hits + (slots - hits) / RB : BLOCKS, listed = SIZED ? slots : ROWS;
   Block* s_blk = reinterpret_cast<Block*>(smem);
@@ -811,9 +814,10 @@ hipError_t decode(const DecodeParams& p, int grid, hipStream_t s) {
     if (p.T <= 16 && (int64_t)std::min(p.NL, p.T * p.k) * (p.f / 16) >= 4 * grid)
       return wide ? run<GRP, 16, 4, 32, 24, 1, 8>(p, grid, s) : run<GRP, 16, 4, 32, 8, 1, 8>(p, grid, s);
     if (p.T <= 16) return wide ? run<GRP, 16, 4, 16, 24, 1, 8>(p, grid, s) : run<GRP, 16, 4, 16, 8, 1, 8>(p, grid, s);
-    // Eight rows a block.  64 tokens of 64 experts (2048 x 1024), of 96 (6144 x 1792)
-    // and of 384, 96 of them here: 134, 462 and 287 us; with four rows 191, 631 and
-    // 287; with twelve, whose sums leave the rings less room, 121, 433 and 313.
+    // Eight rows a block.  In turn on one card, 64 tokens of 64 experts (2048 x 1024), of 96
+    // (6144 x 1792) and of 384, 96 of them here: 139, 461 and 281 us, and 24 tokens 94, 331
+    // and 171; with four rows 196, 617 and 276, 101, 341 and 167; with twelve, whose sums
+    // leave the rings less room, 116, 431 and 284, 96, 336 and 173.
     return wide ? run<GRP, MAX_T, 8, 32, 24, 1, 8>(p, grid, s) : run<GRP, MAX_T, 8, 32, 8, 1, 8>(p, grid, s);
   }
 }
